@@ -60,12 +60,18 @@ class MoEAttnShape(ctypes.Structure):
                 ("head_dim", _I32), ("eps", _F)]
 
 
+class MoEPagedShape(ctypes.Structure):
+    _fields_ = [("requests", _I32), ("tokens", _I32), ("n_head", _I32), ("n_kv_head", _I32), ("head_dim", _I32),
+                ("page_size", _I32), ("pages", _I32), ("max_pages", _I32), ("q_stride", _I32), ("eps", _F)]
+
+
 class MoECacheStats(ctypes.Structure):
     _fields_ = [("steps", _I64), ("hits", _I64), ("misses", _I64), ("evictions", _I64), ("bytes", _I64),
                 ("overflow", _I64)]
 
 
 _SHAPE_P = ctypes.POINTER(MoEShape)
+_PAGED_P = ctypes.POINTER(MoEPagedShape)
 SIGNATURES = {
     "moe_abi_version": (_I32, []),
     "moe_status_string": (ctypes.c_char_p, [_I32]),
@@ -97,6 +103,12 @@ SIGNATURES = {
     "moe_attention_workspace_size": (_SZ, [ctypes.POINTER(MoEAttnShape)]),
     "moe_attention_fwd": (_I32, [ctypes.POINTER(MoEAttnShape), _P, _P, _P, _I32, _P, _P, _SZ, _P]),
     "moe_attention_core": (_I32, [ctypes.POINTER(MoEAttnShape), _P, _P, _P]),
+    "moe_paged_plan": (_I32, [_PAGED_P] + [_P] * 12),
+    "moe_paged_append": (_I32, [_PAGED_P] + [_P] * 6),
+    "moe_paged_attention_workspace_size": (_SZ, [_PAGED_P]),
+    "moe_paged_attention": (_I32, [_PAGED_P] + [_P] * 9 + [_SZ, _P]),
+    "moe_attention_paged_workspace_size": (_SZ, [_PAGED_P, _I32]),
+    "moe_attention_paged_fwd": (_I32, [_PAGED_P, _I32, _P, _P, _P, _I32] + [_P] * 8 + [_SZ, _P]),
     "moe_pack_gate_up": (_I32, [_I32, _I32, _I32, _P, _P, _P, _P]),
     "moe_quantize_int4": (_I32, [_I64, _I32, _P, _P, _P, _P]),
     "moe_device_status": (_I32, [_P, ctypes.POINTER(_I32)]),
@@ -334,6 +346,46 @@ def moe_attention_fwd(shape, x, w_qkv, w_o, residual, out, workspace, stream=Non
 def moe_attention_core(shape, qkv, o, stream=None):
     _check("moe_attention_core", load_library().moe_attention_core(
         ctypes.byref(shape), _ptr(qkv), _ptr(o), _stream(stream)))
+
+
+def make_paged_shape(requests, tokens, n_head, n_kv_head, page_size, pages, max_pages, head_dim=128, q_stride=0,
+                     eps=1e-6) -> MoEPagedShape:
+    return MoEPagedShape(requests, tokens, n_head, n_kv_head, head_dim, page_size, pages, max_pages, q_stride, eps)
+
+
+def moe_paged_plan(shape, ctx_len, new_len, block_table, pool, pool_state_in, pool_state_out, row_start, slot_map,
+                   kv_len, next_ctx, info, stream=None):
+    _check("moe_paged_plan", load_library().moe_paged_plan(
+        ctypes.byref(shape), _ptr(ctx_len), _ptr(new_len), _ptr(block_table), _ptr(pool), _ptr(pool_state_in),
+        _ptr(pool_state_out), _ptr(row_start), _ptr(slot_map), _ptr(kv_len), _ptr(next_ctx), _ptr(info),
+        _stream(stream)))
+
+
+def moe_paged_append(shape, qkv, slot_map, q, k_cache, v_cache, stream=None):
+    _check("moe_paged_append", load_library().moe_paged_append(
+        ctypes.byref(shape), _ptr(qkv), _ptr(slot_map), _ptr(q), _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+
+
+def moe_paged_attention_workspace_size(shape) -> int:
+    return load_library().moe_paged_attention_workspace_size(ctypes.byref(shape))
+
+
+def moe_paged_attention(shape, q, k_cache, v_cache, block_table, row_start, kv_len, out, lse, workspace, stream=None):
+    _check("moe_paged_attention", load_library().moe_paged_attention(
+        ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(row_start), _ptr(kv_len),
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def moe_attention_paged_workspace_size(shape, d) -> int:
+    return load_library().moe_attention_paged_workspace_size(ctypes.byref(shape), d)
+
+
+def moe_attention_paged_fwd(shape, d, x, w_qkv, w_o, residual, k_cache, v_cache, block_table, row_start, slot_map,
+                            kv_len, out, workspace, stream=None):
+    _check("moe_attention_paged_fwd", load_library().moe_attention_paged_fwd(
+        ctypes.byref(shape), d, _ptr(x), _ptr(w_qkv), _ptr(w_o), int(residual), _ptr(k_cache), _ptr(v_cache),
+        _ptr(block_table), _ptr(row_start), _ptr(slot_map), _ptr(kv_len), _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def moe_pack_gate_up(G, width, d, w_gate, w_up, w_gate_up, stream=None):

@@ -296,6 +296,21 @@ cudaError_t launch_qk_norm(uint16_t* qkv, long long rows, int C, int heads, floa
 cudaError_t launch_attention(const uint16_t* qkv, int batch, int seq, int n_head, int n_kv_head, uint16_t* out,
                              cudaStream_t s);
 
+// ---------------------------------------------------------------- paged attention
+// Contracts: moe_paged_shape_t and its calls in moe_gb300.h.
+constexpr int kPagedMaxRequests = 4096;
+cudaError_t launch_paged_plan(const moe_paged_shape_t& s, const int32_t* ctx_len, const int32_t* new_len,
+                              int32_t* block_table, int32_t* pool, const int32_t* pool_in, int32_t* pool_out,
+                              int32_t* row_start, int32_t* slot_map, int32_t* kv_len, int32_t* next_ctx, int32_t* info,
+                              cudaStream_t st);
+cudaError_t launch_paged_append(const moe_paged_shape_t& s, const uint16_t* qkv, const int32_t* slot_map, uint16_t* q,
+                                long long q_stride, uint16_t* k_cache, uint16_t* v_cache, cudaStream_t st);
+size_t paged_attention_scratch_bytes(const moe_paged_shape_t& s);
+cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q, long long q_stride,
+                                   const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* block_table,
+                                   const int32_t* row_start, const int32_t* kv_len, uint16_t* out, float* lse,
+                                   void* scratch, cudaStream_t st);
+
 // ---------------------------------------------------------------- int4 expert cache
 constexpr int kMaxCacheSlots = 256;
 // Device state of the residency cache (least recently used over `slots` HBM slots).

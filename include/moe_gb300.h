@@ -390,6 +390,107 @@ moe_status_t moe_attention_fwd(const moe_attn_shape_t* shape, const void* x, con
                                int32_t residual, void* out, void* workspace, size_t ws_bytes, void* stream);
 moe_status_t moe_attention_core(const moe_attn_shape_t* shape, const void* qkv, void* o, void* stream);
 
+/* Attention over a paged key/value cache: the same block served token by token or in
+ * chunks.  Relay article, opening section, second paragraph (the model is served) and
+ * architecture paragraph (4x grouped-query attention, per-head QK-norm); the article says
+ * nothing about a cache, so its form is this library's: a layer's keys and values live in
+ * pages of page_size tokens,
+ *   k_cache, v_cache [pages][n_kv_head][page_size][128] bf16 (keys after the QK-norm),
+ * and the page with positions [j page_size, (j + 1) page_size) of request r is
+ * block_table[r][j].  A step takes every request's new tokens, rows
+ * [row_start[r], row_start[r + 1]) of a batch of `tokens` rows; rows past
+ * row_start[requests] are padding (a captured graph's fixed row count).  Every length is
+ * read on the device, so a step needs no host round trip and can be captured; one plan
+ * serves all layers, which share block tables and differ in their caches alone.
+ * Supported: 1 <= requests <= 4096, 1 <= tokens <= 2^20, head_dim == 128, n_kv_head >= 1,
+ * n_head % n_kv_head == 0, n_head * 128 <= 8192, page_size in {16, 32, 64, 128},
+ * pages >= 1 with pages * n_kv_head * page_size < 2^31, max_pages >= 1 with
+ * max_pages * page_size <= 2^24, eps > 0, q_stride 0 (dense rows, n_head * 128) or at
+ * least n_head * 128 and a multiple of 8. */
+typedef struct {
+  int32_t requests;   /* rows of the block table, R */
+  int32_t tokens;     /* rows of the batch, T */
+  int32_t n_head, n_kv_head, head_dim;
+  int32_t page_size;  /* tokens per page */
+  int32_t pages;      /* pages of the cache */
+  int32_t max_pages;  /* columns of the block table */
+  int32_t q_stride;   /* elements between query rows; 0 = n_head * 128 */
+  float eps;          /* of the QK-norm */
+} moe_paged_shape_t;
+
+/* One step's bookkeeping, from the requests' lengths, on the device.
+ *   ctx_len   [R] tokens the request already has in the cache
+ *   new_len   [R] its tokens of this step; 0 = none; negative = the request has ended
+ *             and its ceil(ctx_len / page_size) pages go back to the pool
+ *   block_table [R][max_pages] int32, in and out: the entries of pages that a request
+ *             begins in this step are written, all others left as they are
+ *   pool      [pages] int32, in and out: the free pages as a ring; `count` of them from
+ *             place `head` on, cyclically.  Pages are taken from the front in request
+ *             order; returned ones go behind the free ones (in request order, then page
+ *             order) and can be taken from the next call on
+ *   pool_state_in, pool_state_out [2] int32: {head, count} before and after
+ *   row_start [R + 1]: exclusive prefix sum of max(new_len, 0), each at most T
+ *   slot_map  [T]: page * page_size + offset of each row's token; -1 for padding rows
+ *             and for the tokens of a denied request
+ *   kv_len    [R]: keys the request's last token sees: ctx_len + new_len; 0 when denied
+ *             or ended
+ *   next_ctx  [R]: the next step's ctx_len: ctx_len + new_len; ctx_len when denied; 0 when
+ *             ended
+ *   info      [4]: rows in use (row_start[R]), pages taken, pages returned, requests denied
+ * A request with new tokens is denied when the pages wanted by it and the requests before
+ * it are more than `count` (later requests that need no page are still served), or when it
+ * does not fit: ctx_len outside [0, max_pages * page_size], more than max_pages pages, rows
+ * past T.  A request that does not fit asks for no page; that, a pool state outside
+ * [0, pages) x [0, pages] and a table entry in use that is no page set MOE_ERR_DEVICE in the
+ * device status word.  No input but block_table and pool may overlap an output; the outputs
+ * depend on the inputs alone, so the call can be repeated on the same inputs. */
+moe_status_t moe_paged_plan(const moe_paged_shape_t* shape, const int32_t* ctx_len, const int32_t* new_len,
+                            int32_t* block_table, int32_t* pool, const int32_t* pool_state_in,
+                            int32_t* pool_state_out, int32_t* row_start, int32_t* slot_map, int32_t* kv_len,
+                            int32_t* next_ctx, int32_t* info, void* stream);
+
+/* QK-norm of the step's projected rows and the cache write.
+ *   qkv  [T][(n_head + 2 n_kv_head) * 128] bf16: query, key, value heads (the projection)
+ *   q    [T] rows of q_stride bf16: the normalised query heads; may be qkv itself with
+ *        q_stride = (n_head + 2 n_kv_head) * 128, else must not overlap it
+ *   slot_map [T]: rows with a slot outside [0, pages * page_size) are not written to the
+ *        cache (their q is); slots of different rows differ.
+ * Each head is u / sqrt(mean(u^2) + eps) in fp32, rounded once to bf16; values are copied. */
+moe_status_t moe_paged_append(const moe_paged_shape_t* shape, const void* qkv, const int32_t* slot_map, void* q,
+                              void* k_cache, void* v_cache, void* stream);
+
+/* Causal grouped-query attention of every request's new tokens over its pages: the token
+ * of row row_start[r] + i has position p = kv_len[r] - n + i (n = row_start[r + 1] -
+ * row_start[r]) and sees the keys at positions 0 .. p.
+ *   q    [T] rows of q_stride bf16 (normalised query heads)
+ *   out  [T][n_head * 128] bf16
+ *   lse  [T][n_head] fp32: ln of the sum of exp(score), or NULL
+ *   workspace moe_paged_attention_workspace_size(shape) bytes (needs no clearing; calls
+ *        that can overlap must not share it)
+ * Rows without keys (padding rows; all rows of a request with kv_len < n, as a denied one)
+ * get out = 0 and lse = -inf.  What the pages hold past a request's keys is never used,
+ * NaN and infinities included; a non-finite key or value of the request itself may reach
+ * the rows up to 127 positions before it.  row_start is non-decreasing within [0, T] and
+ * kv_len at most max_pages * page_size, else MOE_ERR_DEVICE is set and the rows concerned
+ * are unspecified, as are those of a request with a table entry in use outside [0, pages).
+ * The sums run in an order that depends on the lengths alone: equal calls give equal bits. */
+size_t moe_paged_attention_workspace_size(const moe_paged_shape_t* shape);
+moe_status_t moe_paged_attention(const moe_paged_shape_t* shape, const void* q, const void* k_cache,
+                                 const void* v_cache, const int32_t* block_table, const int32_t* row_start,
+                                 const int32_t* kv_len, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/* The whole block of moe_attention_fwd over a paged cache: projections, moe_paged_append,
+ * moe_paged_attention, output projection and (if residual) x added.  x and out [T][d] bf16,
+ * w_qkv and w_o as for moe_attention_fwd, d % 64 == 0 (64 <= d <= 8192); q_stride is
+ * not read.  The tables are one moe_paged_plan's. */
+size_t moe_attention_paged_workspace_size(const moe_paged_shape_t* shape, int32_t d);
+moe_status_t moe_attention_paged_fwd(const moe_paged_shape_t* shape, int32_t d, const void* x, const void* w_qkv,
+                                     const void* w_o, int32_t residual, void* k_cache, void* v_cache,
+                                     const int32_t* block_table, const int32_t* row_start, const int32_t* slot_map,
+                                     const int32_t* kv_len, void* out, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
 /* Weight preparation, once per weight update and off the hot path: moe_pack_gate_up
  * for every bf16 layer, then moe_quantize_int4 on the packed gate/up and the down
  * weights for int4 serving.

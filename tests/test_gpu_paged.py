@@ -1,0 +1,459 @@
+"""GPU tests of attention over a paged key/value cache against oracle/paged_oracle.py (plain
+loops in 64 bits), through the C ABI.
+
+Tolerances, from the arithmetic alone:
+* plan: whole numbers, equal;
+* append: one rounding to bf16 (2^-8 relative) of a value with a few fp32 roundings (2^-20
+  covers them); values are copied, equal;
+* attention: a score is a sum of 128 products whose absolute values add up to at most
+  sqrt(128) rms(q) rms(k) (Cauchy-Schwarz), each fp32 addition within 2^-23 of that (rounded or
+  cut off): ds = 128 2^-23 sqrt(128) scale^2, scale = the rms of q and of k.  out is rounded
+  once to bf16 (2^-8 |out|), each softmax weight once to bf16 before it multiplies V, and is
+  off by 2 ds from its score and its row's sum (both times the weighted sum of |v|, the
+  oracle's `weight`); fp32 sums and the exponential take 2^-12 weight.  lse: ds, the sum of
+  `keys` exponentials within keys 2^-24 relatively, 2^-20 (1 + |lse|) for exp and log.
+"""
+import numpy as np
+import pytest
+import torch
+
+import aux_loss_free_gb300 as M
+from gpu_util import bf16_to_np
+from oracle import paged_oracle as P
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "the gpu tests need a CUDA device"
+    M.load_library()
+    yield
+    assert M.moe_device_status() == 0
+
+
+def _i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------------------- plan
+
+def _random_step(rng, R, page, max_pages, new, free, pad=0):
+    """Inputs of a step: ctx of every request within its table, its pages at random ids; the
+    pool's ring starts at a random place."""
+    new = np.asarray(new)
+    room = max_pages * page - np.maximum(new, 0)
+    ctx = np.array([rng.integers(0, max(1, m + 1)) for m in room])
+    held = -(-ctx // page)
+    pages = int(held.sum()) + free + 1
+    ids = rng.permutation(pages)
+    table = np.full((R, max_pages), -1)
+    at = 0
+    for r in range(R):
+        table[r, :held[r]] = ids[at:at + held[r]]
+        at += held[r]
+    head = int(rng.integers(0, pages))
+    pool = np.full(pages, -1)
+    pool[(head + np.arange(free)) % pages] = ids[at:at + free]
+    return dict(ctx=ctx, new=new, table=table, pool=pool, state=[head, free], pages=pages,
+                tokens=max(1, int(np.maximum(new, 0).sum()) + pad))
+
+
+def _run_plan(s, page, stream=None):
+    R, max_pages = s["table"].shape
+    shape = M.make_paged_shape(R, s["tokens"], 8, 2, page, s["pages"], max_pages)
+    g = {"block_table": _i32(s["table"]), "pool": _i32(s["pool"])}
+    sizes = dict(pool_state=2, row_start=R + 1, slot_map=s["tokens"], kv_len=R, next_ctx=R, info=4)
+    g.update({k: torch.full((n,), -77, dtype=torch.int32, device=DEV) for k, n in sizes.items()})
+    ins = [_i32(s["ctx"]), _i32(s["new"]), _i32(s["state"])]
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+
+    def call():
+        M.moe_paged_plan(shape, ins[0], ins[1], g["block_table"], g["pool"], ins[2], g["pool_state"], g["row_start"],
+                         g["slot_map"], g["kv_len"], g["next_ctx"], g["info"], stream=stream)
+
+    call()
+    torch.cuda.synchronize()
+    first = {k: v.cpu().numpy().copy() for k, v in g.items()}
+    call()  # the same inputs again: the same outputs
+    torch.cuda.synchronize()
+    for k, v in g.items():
+        assert np.array_equal(v.cpu().numpy(), first[k]), k
+    return first
+
+
+def _check_plan(s, page, stream=None):
+    got = _run_plan(s, page, stream)
+    ref = P.step_plan(s["ctx"], s["new"], s["table"], s["pool"], s["state"], s["tokens"], s["pages"], page)
+    for k, v in ref.items():
+        assert np.array_equal(got[k], v), f"{k}: {got[k]} != {v}"
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("R", [1, 2, 31, 256, 257, 4096])
+def test_plan_matches_oracle(R, page):
+    rng = np.random.default_rng(R * 1000 + page)
+    new = rng.choice([-1, 0, 1, 1, 1, 5, 16, 17, 130], size=R)
+    _check_plan(_random_step(rng, R, page, 12 if R > 300 else 40, new, free=int(R * 12 + 12), pad=R % 3), page)
+
+
+@pytest.mark.parametrize("free", [0, 1, 3, 10, 25])
+def test_plan_denies_what_the_pool_cannot_give(free):
+    rng = np.random.default_rng(free)
+    _check_plan(_random_step(rng, 64, 16, 20, rng.choice([-1, 0, 1, 1, 40], size=64), free=free, pad=5), 16)
+    assert M.moe_device_status() == 0  # a short pool is no error
+
+
+def test_plan_all_ended_all_idle_and_one_long_prompt():
+    rng = np.random.default_rng(3)
+    _check_plan(_random_step(rng, 40, 32, 30, [-1] * 40, free=2), 32)
+    _check_plan(_random_step(rng, 40, 32, 30, [0] * 40, free=0), 32)
+    s = _random_step(rng, 3, 16, 700, [1, 10000, 2], free=700)
+    s["ctx"] = np.array([0, 0, 0])
+    s["table"][:] = -1
+    _check_plan(s, 16)
+
+
+def test_plan_reports_requests_that_do_not_fit():
+    """Longer than the table's row, rows past the batch, a negative context: denied, the
+    others served as if those asked for nothing; MOE_ERR_DEVICE in the status word."""
+    rng = np.random.default_rng(9)
+    for change in ("long", "rows", "negative"):
+        s = _random_step(rng, 6, 16, 8, [1, 1, 20, 1, 3, 1], free=20)
+        if change == "long":
+            s["ctx"][2] = 8 * 16 - 19
+        elif change == "rows":
+            s["tokens"] = 23
+        else:
+            s["ctx"][2] = -1
+        assert M.moe_device_status() == 0
+        _check_plan(s, 16)
+        assert M.moe_device_status() == 6
+    assert M.moe_device_status() == 0
+
+
+def test_plan_reports_bad_pool_states_and_pages():
+    rng = np.random.default_rng(10)
+    for state in ([-1, 2], [1000000, 2], [0, 1000000], [0, -3]):
+        s = _random_step(rng, 3, 16, 8, [40, 1, 0], free=9)
+        s["state"] = state
+        got = _run_plan(s, 16)
+        assert got["info"][1] == 0 and got["kv_len"][0] == 0  # nothing is taken
+        assert M.moe_device_status() == 6
+    s = _random_step(rng, 2, 16, 8, [1, 1], free=9)
+    s["ctx"] = np.array([5, 5])
+    s["table"][:, 0] = [s["pages"], 0]  # no such page
+    got = _run_plan(s, 16)
+    assert got["slot_map"].tolist() == [-1, 5]
+    assert M.moe_device_status() == 6
+
+
+def test_plan_on_another_stream():
+    rng = np.random.default_rng(11)
+    _check_plan(_random_step(rng, 100, 64, 10, rng.choice([-1, 0, 1, 30], size=100), free=300), 64,
+                stream=torch.cuda.Stream())
+
+
+# ----------------------------------------------------------------------------- append
+
+APPEND = [(1, 8, 2, 16, 0), (5, 6, 2, 32, 2), (64, 8, 8, 16, 0), (257, 16, 2, 128, 31), (1000, 4, 1, 64, 0),
+          (33, 64, 1, 16, 1), (40, 1, 1, 64, 0)]
+
+
+def _rows(rng, *shape, scale=1.0):
+    return torch.tensor(rng.standard_normal(shape) * scale, dtype=torch.float32, device=DEV).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,H,KV,page,pad", APPEND)
+@pytest.mark.parametrize("form", ["dense", "strided", "in_place"])
+def test_append_matches_oracle(T, H, KV, page, pad, form):
+    rng = np.random.default_rng(T)
+    pages = T // page + 4
+    slots = np.full(T + pad, -1)
+    slots[:T] = rng.permutation(pages * page)[:T]
+    slots = rng.permutation(slots)
+    qkv = _rows(rng, T + pad, (H + 2 * KV) * 128, scale=3.0)
+    qkv[T // 2] = 0  # a row of zeros: 0 / sqrt(eps)
+    k0, v0 = _rows(rng, pages, KV, page, 128), _rows(rng, pages, KV, page, 128)
+    rq, rk, rv = P.append(bf16_to_np(qkv), slots, H, KV, page, bf16_to_np(k0), bf16_to_np(v0))
+    stride = {"dense": 0, "strided": H * 128 + 24, "in_place": (H + 2 * KV) * 128}[form]
+    shape = M.make_paged_shape(1, T + pad, H, KV, page, pages, 1, q_stride=stride)
+    q = qkv if form == "in_place" else _rows(rng, T + pad, stride or H * 128)
+    was = q.clone()
+    M.moe_paged_append(shape, qkv, _i32(slots), q, k0, v0)
+    torch.cuda.synchronize()
+
+    def near(got, ref):
+        assert (np.abs(got - ref) <= (2.0 ** -8 + 2.0 ** -20) * np.abs(ref)).all()
+
+    near(bf16_to_np(q)[:, :H * 128], rq)
+    assert torch.equal(q[:, H * 128:], was[:, H * 128:])  # nothing beside the query heads is written
+    near(bf16_to_np(k0), rk)
+    assert np.array_equal(bf16_to_np(v0), rv)
+
+
+def test_append_ignores_slots_outside_the_cache():
+    rng = np.random.default_rng(1)
+    shape = M.make_paged_shape(1, 3, 8, 2, 16, 4, 1)
+    k0, v0 = _rows(rng, 4, 2, 16, 128), _rows(rng, 4, 2, 16, 128)
+    k1, v1 = k0.clone(), v0.clone()
+    q = torch.empty(3, 1024, dtype=torch.bfloat16, device=DEV)
+    M.moe_paged_append(shape, _rows(rng, 3, 12 * 128), _i32([64, -5, 2 ** 31 - 1]), q, k0, v0)
+    torch.cuda.synchronize()
+    assert torch.equal(k0, k1) and torch.equal(v0, v1)
+
+
+# -------------------------------------------------------------------------- attention
+
+def _attn_inputs(rng, ctx, new, H, KV, page, pad=0, extra_cols=1, stale=float("nan"), scale=1.0):
+    """A step's tensors; what the pages hold past the requests' keys, and the pages of nobody,
+    is `stale`."""
+    R = len(ctx)
+    kv = np.array(ctx) + np.array(new)
+    held = -(-kv // page)
+    pages = int(held.sum()) + 3
+    ids = rng.permutation(pages)
+    table = np.full((R, int(held.max()) + extra_cols), -1)
+    kc = torch.full((pages, KV, page, 128), stale, dtype=torch.bfloat16, device=DEV)
+    vc = torch.full_like(kc, stale)
+    at = 0
+    for r in range(R):
+        table[r, :held[r]] = ids[at:at + held[r]]
+        at += held[r]
+        pos = np.arange(kv[r])
+        slot_page, off = torch.tensor(table[r][pos // page], device=DEV), torch.tensor(pos % page, device=DEV)
+        k = rng.standard_normal((kv[r], KV, 128)) * scale
+        kc[slot_page, :, off] = torch.tensor(k / np.sqrt((k * k).mean(-1, keepdims=True)) * scale,
+                                             dtype=torch.float32, device=DEV).to(torch.bfloat16)
+        vc[slot_page, :, off] = _rows(rng, kv[r], KV, 128)
+    T = int(np.sum(new)) + pad
+    q = rng.standard_normal((max(T, 1), H, 128))
+    q = torch.tensor(q / np.sqrt((q * q).mean(-1, keepdims=True)) * scale, dtype=torch.float32,
+                     device=DEV).to(torch.bfloat16).reshape(max(T, 1), H * 128)
+    return dict(q=q, k=kc, v=vc, table=table, row_start=np.concatenate([[0], np.cumsum(new)]), kv=kv, H=H, KV=KV,
+                page=page, pages=pages)
+
+
+def _attend(a, stream=None, lse=True, q_stride=0, calls=1):
+    T = a["q"].shape[0]
+    shape = M.make_paged_shape(len(a["kv"]), T, a["H"], a["KV"], a["page"], a["pages"], a["table"].shape[1],
+                               q_stride=q_stride)
+    n = M.moe_paged_attention_workspace_size(shape)
+    ws = torch.randint(0, 256, (n,), dtype=torch.uint8, device=DEV)  # the workspace needs no clearing
+    dev = [_i32(a["table"]), _i32(a["row_start"]), _i32(a["kv"])]
+    outs = []
+    for _ in range(calls):
+        out = torch.full((T, a["H"] * 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        ls = torch.full((T, a["H"]), 7.0, dtype=torch.float32, device=DEV) if lse else None
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        M.moe_paged_attention(shape, a["q"], a["k"], a["v"], *dev, out, ls, ws, stream=stream)
+        torch.cuda.synchronize()
+        outs.append((out, ls))
+    for o, ls in outs[1:]:
+        assert torch.equal(o.view(torch.int16), outs[0][0].view(torch.int16))
+        assert ls is None or torch.equal(ls, outs[0][1])
+    return outs[0]
+
+
+def _check_attention(a, scale=1.0, **kw):
+    T = a["q"].shape[0]
+    out, lse = _attend(a, **kw)
+    q = bf16_to_np(a["q"])[:, :a["H"] * 128]
+    ref = P.paged_attention(q, bf16_to_np(a["k"]), bf16_to_np(a["v"]), a["table"], a["row_start"], a["kv"], a["H"],
+                            a["KV"])
+    got = bf16_to_np(out)
+    ds = 128 * 2.0 ** -23 * np.sqrt(128) * 1.02 * scale * scale  # 1.02: the rms after rounding to bf16
+    bound = 2.0 ** -8 * np.abs(ref["out"]) + (2.0 ** -8 + 2.0 ** -12 + 2 * ds) * ref["weight"]
+    off = np.abs(got - ref["out"])
+    assert np.isfinite(got).all()
+    assert (off <= bound).all(), f"{(off / np.maximum(bound, 1e-30)).max()} times the bound, first row " \
+                                 f"{np.argwhere(off > bound)[0]}"
+    if lse is not None:
+        ls = lse.cpu().numpy().astype(np.float64)
+        empty = np.isneginf(ref["lse"])
+        assert np.array_equal(np.isneginf(ls), empty)
+        keys = int(a["kv"].max())
+        tol = ds + 2.0 ** -24 * keys + 2.0 ** -20 * (1 + np.abs(ref["lse"]))
+        assert (np.abs(ls - ref["lse"])[~empty] <= tol[~empty]).all()
+    # Rows without keys are exactly zero.
+    assert (got.reshape(T, a["H"], 128)[np.isneginf(ref["lse"])] == 0).all()
+
+
+# (ctx, new, n_head, n_kv_head, page, padding rows)
+ATTN = {
+    "one-token-no-context": ([0], [1], 8, 2, 16, 0),
+    "one-token-one-key-before": ([1], [1], 8, 2, 16, 0),
+    "decode-page-and-tile-edges": ([14, 15, 16, 126, 127, 128, 129, 255, 256], [1] * 9, 8, 2, 16, 0),
+    "decode-ragged-64": ([int(x) for x in np.random.default_rng(0).integers(0, 900, 64)], [1] * 64, 8, 2, 32, 3),
+    "decode-long": ([20011], [1], 8, 2, 128, 0),
+    "decode-long-beside-short": ([9000, 3, 0, 700], [1] * 4, 4, 1, 64, 0),
+    "verify-5-groups-of-3": ([0, 7, 123, 1000], [5] * 4, 6, 2, 32, 7),
+    "prompt-one-tile": ([0], [128], 8, 2, 64, 0),
+    "prompt-odd": ([0], [333], 8, 2, 16, 1),
+    "prompts-ragged": ([0, 0, 0], [1, 130, 70], 8, 2, 128, 0),
+    "chunk-over-context": ([1000], [200], 8, 2, 32, 0),
+    "chunk-many-rows": ([77, 513], [257, 64], 4, 1, 16, 5),
+    "no-grouping": ([40, 300], [100, 1], 4, 4, 16, 0),
+    "no-grouping-long-chunk": ([5], [400], 2, 2, 64, 0),
+    "groups-of-5": ([200, 3], [70, 1], 5, 1, 64, 0),
+    "groups-of-7": ([64], [39], 14, 2, 16, 0),
+    "one-shared-head-of-16": ([100, 600], [33, 1], 16, 1, 32, 0),
+    "one-shared-head-of-64": ([50, 10], [9, 1], 64, 1, 16, 0),
+    "one-head": ([300], [150], 1, 1, 128, 2),
+    "mixed-step": ([700, 0, 64, 1, 2000, 0], [1, 180, 1, 40, 1, 1], 8, 2, 16, 40),
+    "idle-requests-between": ([100, 50, 7, 0, 90], [1, 0, 3, 0, 1], 8, 2, 16, 2),
+}
+
+
+@pytest.mark.parametrize("name", ATTN)
+def test_attention_matches_oracle(name):
+    ctx, new, H, KV, page, pad = ATTN[name]
+    _check_attention(_attn_inputs(np.random.default_rng(len(name)), ctx, new, H, KV, page, pad), calls=2)
+
+
+@pytest.mark.parametrize("stale", [float("inf"), -float("inf"), 3e38])
+def test_attention_never_uses_what_lies_past_the_keys(stale):
+    rng = np.random.default_rng(2)
+    _check_attention(_attn_inputs(rng, [130, 9, 0], [1, 40, 1], 8, 2, 64, 1, stale=stale))
+
+
+def test_attention_of_denied_requests_and_padding_is_zero():
+    a = _attn_inputs(np.random.default_rng(4), [50, 300, 20, 10], [1, 70, 2, 1], 8, 2, 16, pad=300)
+    a["kv"][[1, 3]] = 0  # denied: no keys, whatever the rows
+    _check_attention(a)
+    a["kv"][:] = 0  # no row of the batch has keys
+    _check_attention(a)
+
+
+def test_attention_with_large_scores():
+    """Rows whose softmax is a near one-hot, and running maxima that keep growing: scores up
+    to 16 x 16 x sqrt(128)."""
+    rng = np.random.default_rng(6)
+    a = _attn_inputs(rng, [900, 0], [1, 300], 8, 2, 16, scale=16.0)
+    _check_attention(a, scale=16.0)
+    # Keys that grow along the sequence: every tile raises the maximum.
+    a = _attn_inputs(rng, [1500], [40], 4, 1, 64)
+    pos = np.arange(1540)
+    ids, off = torch.tensor(a["table"][0][pos // 64], device=DEV), torch.tensor(pos % 64, device=DEV)
+    a["k"][ids, :, off] = (a["q"][-1, :128][None, None] * torch.linspace(0.01, 4, 1540, device=DEV)[:, None, None]
+                           ).to(torch.bfloat16)
+    _check_attention(a, scale=4.0)
+
+
+def test_attention_reads_strided_queries_and_skips_lse():
+    rng = np.random.default_rng(7)
+    a = _attn_inputs(rng, [40, 200], [70, 1], 8, 2, 16, 2)
+    wide = _rows(rng, a["q"].shape[0], 12 * 128)
+    wide[:, :8 * 128] = a["q"]
+    a["q"] = wide
+    _check_attention(a, q_stride=12 * 128, lse=False)
+
+
+def test_attention_on_another_stream():
+    a = _attn_inputs(np.random.default_rng(8), [40, 2000], [70, 1], 8, 2, 16, 2)
+    _check_attention(a, stream=torch.cuda.Stream(), calls=3)
+
+
+def test_attention_far_into_a_large_cache():
+    """Pages whose elements lie past 2^31 and 2^32: 32-bit element offsets would wrap."""
+    KV, page, pages = 2, 128, 140000  # 2 x 9.2 GB, 4.6e9 elements each
+    k = torch.empty(pages, KV, page, 128, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    a = _attn_inputs(np.random.default_rng(12), [300, 100], [40, 1], 8, 2, page)
+    small_k, small_v = a["k"], a["v"]
+    far = np.array([pages - 1, 70000, 139000, 65536, 131072, 3, 100000, 99999])[:a["pages"]]
+    for i, f in enumerate(far):
+        k[f], v[f] = small_k[i], small_v[i]
+    T = a["q"].shape[0]
+    ref_out, ref_lse = _attend(a)
+    table = np.where(a["table"] >= 0, far[a["table"]], -1)
+    big = dict(a, k=k, v=v, table=table, pages=pages)
+    out, lse = _attend(big)
+    assert torch.equal(out.view(torch.int16), ref_out.view(torch.int16)) and torch.equal(lse, ref_lse)
+    # The write side at the same places.
+    shape = M.make_paged_shape(1, T, 8, KV, page, pages, 1)
+    slots = far[np.arange(T) % len(far)].astype(np.int64) * page + np.arange(T) // len(far)
+    qkv = _rows(np.random.default_rng(13), T, 12 * 128)
+    M.moe_paged_append(shape, qkv, _i32(slots), torch.empty(T, 1024, dtype=torch.bfloat16, device=DEV), k, v)
+    torch.cuda.synchronize()
+    st = torch.tensor(slots, device=DEV)
+    assert torch.equal(v[st // page, :, st % page].reshape(T, -1), qkv[:, 10 * 128:])
+
+
+def test_attention_reports_tables_and_lengths_out_of_range():
+    """A table entry that is no page, lengths past the table: status MOE_ERR_DEVICE, the other
+    requests' rows as they should be."""
+    rng = np.random.default_rng(14)
+    a = _attn_inputs(rng, [100, 40], [1, 3], 8, 2, 16)
+    ref, _ = _attend(a)
+    for change in ("page", "negative", "kv"):
+        b = dict(a, table=a["table"].copy(), kv=a["kv"].copy())
+        if change == "kv":
+            b["kv"][0] = 16 * b["table"].shape[1] + 1
+        else:
+            b["table"][0, 2] = a["pages"] if change == "page" else -1
+        assert M.moe_device_status() == 0
+        out, _ = _attend(b)
+        assert M.moe_device_status() == 6
+        assert torch.equal(out[1:].view(torch.int16), ref[1:].view(torch.int16))
+
+
+def test_plan_append_attention_in_a_captured_graph():
+    """One step captured once and replayed with other lengths and rows in the same buffers."""
+    rng = np.random.default_rng(15)
+    H, KV, page, R, T, pages, width = 8, 2, 16, 4, 96, 64, 12
+    shape = M.make_paged_shape(R, T, H, KV, page, pages, width)
+    k = torch.full((pages, KV, page, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    v = torch.full_like(k, float("nan"))
+    ctx, new = _i32([0] * R), _i32([1] * R)
+    table, pool = torch.full((R, width), -1, dtype=torch.int32, device=DEV), _i32(rng.permutation(pages))
+    state, nxt, info = _i32([0, pages]), torch.empty(R, dtype=torch.int32, device=DEV), _i32([0] * 4)
+    state_out, rs, slot, kv = _i32([0, 0]), _i32([0] * (R + 1)), _i32([0] * T), _i32([0] * R)
+    qkv, q = _rows(rng, T, (H + 2 * KV) * 128), torch.empty(T, H * 128, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    ws = torch.empty(M.moe_paged_attention_workspace_size(shape), dtype=torch.uint8, device=DEV)
+
+    def step(stream):
+        M.moe_paged_plan(shape, ctx, new, table, pool, state, state_out, rs, slot, kv, nxt, info, stream=stream)
+        M.moe_paged_append(shape, qkv, slot, q, k, v, stream=stream)
+        M.moe_paged_attention(shape, q, k, v, table, rs, kv, out, None, ws, stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(side)  # warm, outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(side)
+    table.fill_(-1)
+    hist = {r: [] for r in range(R)}
+    for lens in ([60, 0, 3, 33], [1, 17, 1, 1], [1, 1, 50, 1], [1, 1, 1, 20]):
+        rows = _rows(rng, T, (H + 2 * KV) * 128)
+        qkv.copy_(rows)
+        new.copy_(_i32(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        u = bf16_to_np(rows).reshape(T, H + 2 * KV, 128)
+        at = 0
+        for r, n in enumerate(lens):
+            hist[r] += list(u[at:at + n])
+            if n:
+                seq = np.stack(hist[r])
+                qn, kn, vn = P.append(seq.reshape(len(seq), -1), np.arange(len(seq)), H, KV, len(seq),
+                                      np.zeros((1, KV, len(seq), 128)), np.zeros((1, KV, len(seq), 128)))
+                ref = P.paged_attention(qn[-n:], kn, vn, np.array([[0]]), np.array([0, n]), np.array([len(seq)]), H, KV)
+                got = bf16_to_np(out)[at:at + n]
+                # q and k are rounded to bf16 here and not in the reference: scores move by at
+                # most 2 x 2^-8 x sqrt(128) < 0.09 each, the weights by that share.
+                assert (np.abs(got - ref["out"]) <= 2.0 ** -8 * np.abs(ref["out"]) + 0.2 * ref["weight"]).all()
+                rel = np.linalg.norm(got - ref["out"]) / np.linalg.norm(ref["out"])
+                assert rel <= 2e-2
+            at += n
+        ctx.copy_(nxt)
+        state.copy_(state_out)
+        assert (bf16_to_np(out)[at:] == 0).all()
