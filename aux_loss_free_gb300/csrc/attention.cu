@@ -68,40 +68,6 @@ struct AttnParams {
   float scale_log2;  // log2(e) / sqrt(HD)
 };
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// D[tmem] (+)= A[tmem] * B[smem], one 128 x N x 16 step with A read from tensor memory:
-// row m of A in lane m, two bf16 values per 32-bit column (the even k in the low half).
-__device__ __forceinline__ void tc_mma_bf16_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                   uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// 2^x by the hardware's approximate base-2 exponential (relative error near 2^-22;
-// 2^-inf = 0).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -435,6 +401,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 }  // namespace
 
+bool encode_tma_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
+  const auto fn = encode_fn();
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_qk_norm(uint16_t* qkv, long long rows, int C, int heads, float eps, cudaStream_t s) {
   if (rows == 0 || heads == 0) return cudaSuccess;
   return launch_pdl(qk_norm_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, qkv, rows, C, heads, eps);
@@ -444,19 +419,12 @@ cudaError_t launch_attention(const uint16_t* qkv, int batch, int seq, int n_head
                              cudaStream_t s) {
   AttnParams p;
   std::memset(&p, 0, sizeof(p));
-  auto fn = encode_fn();
-  if (!fn) return cudaErrorInvalidValue;
   const long long T = (long long)batch * seq;
   const int C = (n_head + 2 * n_kv_head) * HD;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(AT), static_cast<cuuint64_t>(T),
-                              static_cast<cuuint64_t>(C / AT)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(C) * 2, static_cast<cuuint64_t>(AT) * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(AT), static_cast<cuuint32_t>(BQ), 2};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  if (fn(&p.qkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(qkv), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  const uint64_t dims[3] = {AT, (uint64_t)T, (uint64_t)(C / AT)};
+  const uint64_t strides[2] = {(uint64_t)C * 2, (uint64_t)AT * 2};
+  const uint32_t box[3] = {AT, BQ, 2};
+  if (!encode_tma_bf16(&p.qkv, qkv, 3, dims, strides, box)) return cudaErrorInvalidValue;
   p.out = out;
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInvalidDevicePointer;

@@ -296,6 +296,11 @@ cudaError_t launch_qk_norm(uint16_t* qkv, long long rows, int C, int heads, floa
 cudaError_t launch_attention(const uint16_t* qkv, int batch, int seq, int n_head, int n_kv_head, uint16_t* out,
                              cudaStream_t s);
 
+// TMA descriptor of a bf16 tensor of `rank` dimensions (sizes and box in elements,
+// innermost first; strides of dimensions 1.. in bytes), 128-byte swizzle.
+bool encode_tma_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box);
+
 // ---------------------------------------------------------------- paged attention
 // Contracts: moe_paged_shape_t and its calls in moe_gb300.h.
 constexpr int kPagedMaxRequests = 4096;

@@ -1,9 +1,44 @@
-// Causal grouped-query attention of a step's new tokens over a paged key/value cache.
+// Causal grouped-query attention of a step's new tokens over a paged key/value cache, on
+// tcgen05 tensor cores (sm_103a).
 //
-// Simple form: one warp per (token row, query head), four of the head's 128 values per
-// lane, one pass over the keys with the running maximum and sum of the softmax.
+// Relay article ("Una carrera de relevos con GPUs alquiladas entrenó el MoE de 2.7B de
+// NanoColibri por $200"), opening section, architecture paragraph: grouped-query attention;
+// the paged cache is this library's own form.
+//
+// Rows.  The query heads of one key/value head see the same keys, so a tile of queries packs
+// them: row m of a 128-row half tile is token m / G, head m % G of the group (G query heads
+// per key/value head, tq = 128 / (G rounded up to a power of two) tokens).  One decode token
+// fills G rows, a chunk fills all of them, and every key tile is loaded once per group.  A
+// work tile is two halves (2 tq tokens): with tokens in both ("pair") the halves share the key
+// and value tiles and keep the tensor cores busy in turn; with tokens in the first half only
+// ("single") one half's score buffers alternate between key tiles.
+//
+// Work.  The unit is one 128-key tile of one work tile.  All units of the call, in order
+// (request, key/value head, query tile, key tile), are split into equal contiguous ranges, one
+// per CTA, whatever the requests' lengths: a range holds the end of one work tile, whole work
+// tiles and the beginning of another.  A work tile that does not lie in one range leaves
+// partial outputs, which paged_combine_kernel joins in the order of the keys.  Every CTA
+// computes the ranges itself from the lengths (one prefix sum over the requests), so the call
+// needs no plan, no counters and no cleared workspace.  Rows that belong to no request are the
+// rows of one more request without keys; their units read nothing and give zeros.
+//
+// paged_attention_kernel, one CTA per SM, 10 warps:
+//   - warp 8 walks the CTA's range, publishes each item (work tile, key tiles) in a small
+//     ring, and issues the TMA copies: the query halves, and one box per page and 64-column
+//     half of the key and value tiles, into a ring of five 32 KB stages;
+//   - warp 9 (one thread) issues tcgen05.mma: S = Q K^T into a score buffer, O += P V with P
+//     (bf16) read from the score buffer's own columns.  The pipe runs in order, so a score
+//     product that overwrites a buffer needs no wait for the product that read P from it;
+//   - warps 0-3 and 4-7 (one query row per thread, its TMEM lane): the online softmax in the
+//     log2 domain on 128 scores held in registers, O rescaled only when the row's maximum
+//     grew by more than 8 (2^8); at the end O / l, or O, m and l as a partial.
+// Values past the last key that a tile may see are zeroed in shared memory before P V: their
+// weight is 0, but 0 times a stale NaN or infinity is not.
+// Every barrier wait is bounded; on a timeout the status word is set and the CTA exits.
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <cstring>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -11,100 +46,771 @@
 namespace moe {
 namespace {
 
-constexpr unsigned FULL = 0xFFFFFFFFu;
 constexpr int HD = kAttnHeadDim;
+constexpr int BK = 128;                       // keys per tile
+constexpr int ATOM_BYTES = 128 * 64 * 2;      // 16 KB: 128 rows x 64 bf16, 128-byte swizzle
+constexpr int TILE_BYTES = 2 * ATOM_BYTES;    // 32 KB: 128 rows x 128
+constexpr int STAGES = 5;                     // key and value tiles in flight: K0 V0 K1 V1 ...
+constexpr int RING_OFF = 2 * TILE_BYTES;      // after the two query halves
+constexpr int SMEM_BYTES = RING_OFF + STAGES * TILE_BYTES + 1024;
+constexpr int THREADS = 320;
+constexpr int WARPS = THREADS / 32;
+constexpr int ITEMS = 4;                      // depth of the item ring
+constexpr int CTAS = 152;                     // one per SM
+constexpr uint32_t O_COL = 256;               // score buffers at 0 and 128, outputs at 256 and 384
+constexpr uint32_t TMEM_COLS = 512;
+constexpr unsigned FULL = 0xFFFFFFFFu;
+constexpr float LN2 = 0.6931471805599453f;
+
+// Partials: per CTA two slots (a work tile continued from the range before; one that goes on in
+// the next range), each O [32][256] float4 (columns by four, then rows: coalesced over the
+// rows) and m, l [256].
+constexpr size_t PART_O = 32 * 256 * 16;
+constexpr size_t PART_BYTES = PART_O + 2 * 256 * 4;
+
+// One work tile that goes on past the range of the CTA that begins it.
+struct Split {
+  int row0, ntok, g, last;  // first token row, tokens, key/value head, last CTA with a part (-1: none)
+};
+constexpr size_t SCRATCH_BYTES = CTAS * sizeof(Split) + 2 * CTAS * PART_BYTES;
 
 struct PagedParams {
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
+  CUtensorMap q;  // [T] rows viewed as (64, 2, n_head, T), box (64, 1, G, tq)
+  CUtensorMap k;  // cache viewed as (64, rows, 2), box (64, page, 1)
+  CUtensorMap v;
   const int32_t* table;
   const int32_t* row_start;
   const int32_t* kv_len;
   uint16_t* out;
   float* lse;
+  Split* splits;
+  uint8_t* parts;
   int* status;
-  long long q_stride;
-  int R, T, n_head, n_kv_head, pages, max_pages, page_shift;
-  float scale;
+  int R, T, n_head, n_kv_head, G, tq, pages, max_pages, page_shift;
+  float scale_log2;  // log2(e) / sqrt(HD)
 };
 
-__device__ __forceinline__ float4 load4(const uint16_t* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xFFFF0000u));
+struct Item {
+  int row0, ntok;   // first token row and tokens of the work tile
+  int pos0;         // position of its first token
+  int kvlim;        // keys that its last token sees; 0 = a request without keys
+  int j0, nt;       // first key tile, key tiles of this item; nt == 0 ends the walk
+  int g, half;      // key/value head; query half of a single tile, 2 = pair
+  int part;         // -1 = the whole work tile, else the partial slot
+};
+
+// One request's work tiles.
+struct Request {
+  int row0, n, ctx;   // first row, new tokens, keys before them
+  bool dead;          // no keys: one unit per work tile
+  int qn;             // work tiles per key/value head
+};
+
+__device__ __forceinline__ long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// Request r; r == R is the padding rows.  Lengths out of range are reported once per call
+// (`report`) and leave a request without keys or without rows.
+__device__ Request load_request(const PagedParams& p, int r, bool report) {
+  Request q;
+  const int a = p.row_start[r], b = r < p.R ? p.row_start[r + 1] : p.T;
+  const bool rows_ok = a >= 0 && a <= b && b <= p.T;
+  const int kv = r < p.R ? p.kv_len[r] : 0;
+  const bool kv_ok = kv <= (p.max_pages << p.page_shift);
+  if (report && !(rows_ok && kv_ok)) atomicOr(p.status, kDevCheck);
+  q.row0 = a;
+  q.n = rows_ok ? b - a : 0;
+  q.dead = !kv_ok || kv < q.n || r == p.R;
+  q.ctx = q.dead ? 0 : kv - q.n;
+  const int tQ = 2 * p.tq;
+  q.qn = (q.n + tQ - 1) / tQ;
+  return q;
 }
 
-__global__ void paged_attention_kernel(const PagedParams p) {
+// Units of the request's first k work tiles, all full (2 tq tokens): tile i reaches position
+// ctx + (i + 1) 2 tq.  With 2 tq dividing 128, ceil((ctx + (i + 1) tQ) / 128) =
+// ceil((c0 + i + 1) / P) for c0 = ceil(ctx / tQ) and P = 128 / tQ, and the sum over i is a
+// difference of sums of ceil(m / P); with 2 tq = 256 a tile adds two key tiles to the last.
+__device__ long long units_of_full(const Request& q, long long k, int tQ) {
+  if (q.dead) return k;
+  if (tQ > BK) return k * (k + 1) + k * cdiv(q.ctx, BK);
+  const long long P = BK / tQ, c0 = cdiv(q.ctx, tQ);
+  auto sum = [P](long long n) {
+    const long long d = n / P, rem = n - d * P;
+    return P * (d * (d + 1) / 2) + rem * (d + 1);
+  };
+  return sum(c0 + k) - sum(c0);
+}
+__device__ __forceinline__ int tile_units(const Request& q, int i, int tQ) {
+  return q.dead ? 1 : (int)cdiv(q.ctx + min(q.n, (i + 1) * tQ), BK);
+}
+// Units of one key/value head of the request.
+__device__ long long head_units(const Request& q, int tQ) {
+  if (q.qn == 0) return 0;
+  return units_of_full(q, q.qn - 1, tQ) + tile_units(q, q.qn - 1, tQ);
+}
+
+struct SmemState {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t ring_full[STAGES], ring_empty[STAGES];
+  uint64_t s_full[4];    // pair: half 0, 1; single: even, odd key tile
+  uint64_t p_full[4];
+  uint64_t pv_done[2];   // single: even, odd key tile
+  uint64_t o_full[2];
+  uint64_t item_full[ITEMS], item_empty[ITEMS];
+  Item items[ITEMS];
+  long long warp_sum[WARPS];
+  long long start_off;   // units of the starting request before the range
+  int start_req;
+  uint32_t tmem;
+};
+
+// Warp-wide wait by lane 0.
+__device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, int* status) {
+  int w = 1;
+  if (threadIdx.x % 32 == 0) w = mbar_wait(smem_u32(bar), parity & 1u, status) ? 1 : 0;
+  w = __shfl_sync(FULL, w, 0);
+  __syncwarp();  // what lane 0 acquired is every lane's
+  return w != 0;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) SmemState sm;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tQ = 2 * p.tq;
+
+  if (warp == 8 && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_full[i]), 1);
+      mbar_init(smem_u32(&sm.q_empty[i]), 1);
+      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+      mbar_init(smem_u32(&sm.o_full[i]), 1);
+    }
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&sm.ring_full[i]), 1);
+      mbar_init(smem_u32(&sm.ring_empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
+    }
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(smem_u32(&sm.item_full[i]), 1);
+      mbar_init(smem_u32(&sm.item_empty[i]), 9);  // the issuer and eight softmax warps
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&p.q);
+    tma_prefetch_desc(&p.k);
+    tma_prefetch_desc(&p.v);
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&sm.tmem), TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();  // lengths, tables, queries and pages come from earlier kernels
+  pdl_trigger();
+
+  // ---------------------------------------------------------------- this CTA's range
+  const int nreq = p.R + 1;  // the padding rows last
+  const int per = (nreq + THREADS - 1) / THREADS;
+  const int r0 = min(nreq, tid * per), r1 = min(nreq, r0 + per);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += head_units(load_request(p, r, blockIdx.x == 0), tQ) * p.n_kv_head;
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(FULL, upto, o);
+    if (lane >= o) upto += up;
+  }
+  if (lane == 31) sm.warp_sum[warp] = upto;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) upto += sm.warp_sum[w];
+    total += sm.warp_sum[w];
+  }
+  const int ctas = (int)min((long long)gridDim.x, total);  // every range holds a unit
+  const int c = blockIdx.x;
+  const bool working = c < ctas;
+  const long long u0 = working ? total * c / ctas : 0, u1 = working ? total * (c + 1) / ctas : 0;
+  if (working && mine > 0 && u0 >= upto - mine && u0 < upto) {
+    long long at = upto - mine;
+    for (int r = r0; r < r1; ++r) {
+      const long long w = head_units(load_request(p, r, false), tQ) * p.n_kv_head;
+      if (u0 < at + w) {
+        sm.start_req = r;
+        sm.start_off = u0 - at;
+        break;
+      }
+      at += w;
+    }
+  }
+  if (tid == 0) p.splits[c].last = -1;
+  __syncthreads();
+  const uint32_t tmem = sm.tmem;
+
+  if (!working) {
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ walk and TMA copies
+    const int nb = BK >> p.page_shift;         // pages per key tile
+    const int box = lane & (nb - 1), col = lane >= nb ? 1 : 0;
+    const bool copies = lane < 2 * nb;
+    const uint32_t box_dst = col * ATOM_BYTES + (box << p.page_shift) * 128;
+    const uint32_t q_bytes = (uint32_t)(2 * p.tq * p.G * 128);
+    const int rows_end = (int)((long long)p.pages * p.n_kv_head << p.page_shift);  // out of range: zeros
+    int r = sm.start_req;
+    Request q = load_request(p, r, false);
+    long long w = head_units(q, tQ);
+    int g = (int)(sm.start_off / w);
+    const long long off = sm.start_off - g * w;
+    int i = 0;  // the work tile that holds unit `off` of the head: units_of_full(i) <= off
+    {
+      int hi = q.qn;
+      while (hi - i > 1) {
+        const int mid = (i + hi) >> 1;
+        if (units_of_full(q, mid, tQ) <= off) i = mid;
+        else hi = mid;
+      }
+    }
+    int j = (int)(off - units_of_full(q, i, tQ));
+    long long left = u1 - u0, unit = u0;
+    uint32_t items = 0, loads = 0, q_uses[2] = {0, 0};
+    int next_half = 0;
+    bool ok = true;
+    while (ok) {
+      Item it;
+      it.nt = 0;
+      int tile_n = 0;
+      if (left > 0) {
+        tile_n = tile_units(q, i, tQ);
+        it.row0 = q.row0 + i * tQ;
+        it.ntok = min(tQ, q.n - i * tQ);
+        it.pos0 = q.ctx + i * tQ;
+        it.kvlim = q.dead ? 0 : it.pos0 + it.ntok;
+        it.j0 = j;
+        it.nt = (int)min((long long)(tile_n - j), left);
+        it.g = g;
+        it.half = it.ntok > p.tq ? 2 : next_half;
+        const bool ends = j + it.nt == tile_n;
+        it.part = j == 0 && ends ? -1 : (j == 0 ? 2 * c + 1 : 2 * c);
+        if (j == 0 && !ends && lane == 0) {
+          // The unit after the tile's last one belongs to CTA ((u + 1) ctas - 1) / total.
+          const long long end = unit + tile_n;
+          Split s;
+          s.row0 = it.row0;
+          s.ntok = it.ntok;
+          s.g = g;
+          s.last = (int)((end * ctas - 1) / total);
+          p.splits[c] = s;
+        }
+      }
+      const int slot = items % ITEMS;
+      if (!warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status)) break;
+      if (lane == 0) {
+        sm.items[slot] = it;
+        mbar_arrive(smem_u32(&sm.item_full[slot]));
+      }
+      __syncwarp();
+      ++items;
+      if (it.nt == 0) break;
+
+      // The query halves.
+      for (int h = 0; h < 2; ++h) {
+        if (it.half != 2 && it.half != h) continue;
+        if (!warp_wait(&sm.q_empty[h], q_uses[h] ^ 1u, p.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sm.q_full[h]);
+          mbar_arrive_expect_tx(bar, q_bytes);
+          const int tok = it.row0 + (it.half == 2 ? h * p.tq : 0);
+          tma_load_4d(base + h * TILE_BYTES, &p.q, bar, 0, 0, g * p.G, tok);
+          tma_load_4d(base + h * TILE_BYTES + ATOM_BYTES, &p.q, bar, 0, 1, g * p.G, tok);
+        }
+        ++q_uses[h];
+      }
+      if (!ok) break;
+      if (it.half != 2) next_half = it.half ^ 1;
+
+      // The key and value tiles, one box per page and column half and lane.
+      const int32_t* const row = p.table + (long long)r * p.max_pages;
+      for (int t = 0; t < it.nt && ok; ++t) {
+        const int page = (it.j0 + t) * nb + box;
+        int coord = rows_end;
+        if (copies && ((long long)page << p.page_shift) < it.kvlim) {
+          const int id = row[page];
+          if (id >= 0 && id < p.pages) coord = (id * p.n_kv_head + g) << p.page_shift;
+          else atomicOr(p.status, kDevCheck);
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int st = loads % STAGES;
+          if (!warp_wait(&sm.ring_empty[st], (loads / STAGES) ^ 1u, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&sm.ring_full[st]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, TILE_BYTES);
+          __syncwarp();
+          if (copies)
+            tma_load_3d(base + RING_OFF + st * TILE_BYTES + box_dst, kv ? &p.v : &p.k, bar, 0, coord, col);
+          ++loads;
+        }
+      }
+      left -= it.nt;
+      unit += it.nt;
+      // The next work tile: query tile, then head, then request.
+      if (left > 0) {
+        j = 0;
+        if (++i == q.qn) {
+          i = 0;
+          if (++g == p.n_kv_head) {
+            g = 0;
+            do q = load_request(p, ++r, false);
+            while (q.qn == 0);
+          }
+        }
+      }
+    }
+    // No copy may still be landing when the CTA exits.
+    for (int h = 0; h < 2; ++h)
+      if (q_uses[h]) warp_wait(&sm.q_full[h], q_uses[h] - 1, p.status);
+    for (uint32_t l = loads > STAGES ? loads - STAGES : 0; l < loads; ++l)
+      warp_wait(&sm.ring_full[l % STAGES], l / STAGES, p.status);
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16_f32(128, BK, 0, 0);
+      constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, 0, 1);
+      uint32_t q_uses[2] = {0, 0}, tiles = 0, pairs = 0, singles[2] = {0, 0};
+      auto wait = [&](const uint64_t* bar, uint32_t parity) {
+        return mbar_wait_spin(smem_u32(bar), parity & 1u, p.status);
+      };
+      auto score = [&](int half, int buf, int st) {  // S[buf] = Q[half] K^T
+        const uint64_t qd = sw128_kmajor_desc(base + half * TILE_BYTES);
+        const uint64_t kd = sw128_kmajor_desc(base + RING_OFF + st * TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          tc_mma_bf16(tmem + buf * BK, qd + (kk >> 2) * (ATOM_BYTES >> 4) + 2 * (kk & 3),
+                      kd + (kk >> 2) * (ATOM_BYTES >> 4) + 2 * (kk & 3), id_s, kk != 0);
+      };
+      auto value = [&](int out, int buf, int st, bool first) {  // O[out] (+)= P[buf] V
+        const uint64_t vd = sw128_mnmajor_desc(base + RING_OFF + st * TILE_BYTES, ATOM_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma_bf16_a_tmem(tmem + O_COL + out * HD, tmem + buf * BK + kk * 8, vd + kk * 128u, id_pv,
+                             !first || kk != 0);
+      };
+      for (uint32_t items = 0;; ++items) {
+        const int slot = items % ITEMS;
+        if (!wait(&sm.item_full[slot], items / ITEMS)) break;
+        const int nt = sm.items[slot].nt, half = sm.items[slot].half;
+        mbar_arrive(smem_u32(&sm.item_empty[slot]));
+        if (nt == 0) break;
+        const bool pair = half == 2;
+        bool ok = true;
+        for (int h = 0; h < 2 && ok; ++h)
+          if (pair || half == h) ok = wait(&sm.q_full[h], q_uses[h]++);
+        // Key tile t of the item is load 2 (tiles + t), its value tile the next one.
+        auto ready = [&](int t, int kv) {
+          const uint32_t l = 2 * (tiles + t) + kv;
+          return wait(&sm.ring_full[l % STAGES], l / STAGES);
+        };
+        auto stage = [&](int t, int kv) { return (int)((2 * (tiles + t) + kv) % STAGES); };
+        if (!ok || !ready(0, 0)) break;
+        tc_fence_after();
+        if (pair) {
+          for (int h = 0; h < 2; ++h) {
+            score(h, h, stage(0, 0));
+            tc_commit(smem_u32(&sm.s_full[h]));
+          }
+          tc_commit(smem_u32(&sm.ring_empty[stage(0, 0)]));
+          for (int t = 0; t < nt && ok; ++t) {
+            const bool more = t + 1 < nt;
+            for (int h = 0; h < 2; ++h) {
+              if (!wait(&sm.p_full[h], pairs + t) || (h == 0 && !ready(t, 1))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              value(h, h, stage(t, 1), t == 0);
+              if (h == 1) tc_commit(smem_u32(&sm.ring_empty[stage(t, 1)]));
+              if (more) {
+                if (h == 0 && !ready(t + 1, 0)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                score(h, h, stage(t + 1, 0));
+                tc_commit(smem_u32(&sm.s_full[h]));  // covers the value product before it
+                if (h == 1) tc_commit(smem_u32(&sm.ring_empty[stage(t + 1, 0)]));
+              } else {
+                tc_commit(smem_u32(&sm.o_full[h]));
+                if (h == 1)
+                  for (int x = 0; x < 2; ++x) tc_commit(smem_u32(&sm.q_empty[x]));
+              }
+            }
+          }
+          pairs += nt;
+        } else {
+          score(half, 0, stage(0, 0));
+          tc_commit(smem_u32(&sm.s_full[2]));
+          tc_commit(smem_u32(&sm.ring_empty[stage(0, 0)]));
+          for (int t = 0; t < nt; ++t) {
+            const int b = t & 1;
+            if (t + 1 < nt) {
+              if (!ready(t + 1, 0)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              score(half, b ^ 1, stage(t + 1, 0));
+              tc_commit(smem_u32(&sm.s_full[2 + (b ^ 1)]));
+              tc_commit(smem_u32(&sm.ring_empty[stage(t + 1, 0)]));
+            }
+            if (t + 1 == nt) tc_commit(smem_u32(&sm.q_empty[half]));  // every score product is issued
+            if (!wait(&sm.p_full[2 + b], singles[b] + (t >> 1)) || !ready(t, 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            value(0, b, stage(t, 1), t == 0);
+            tc_commit(smem_u32(&sm.ring_empty[stage(t, 1)]));
+            tc_commit(smem_u32(&sm.pv_done[b]));
+            if (t + 1 == nt) tc_commit(smem_u32(&sm.o_full[0]));
+          }
+          singles[0] += (nt + 1) >> 1;
+          singles[1] += nt >> 1;
+        }
+        if (!ok) break;
+        tiles += nt;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    const int wg = warp >> 2, q4 = warp & 3;
+    const int m_row = q4 * 32 + lane;              // row of the half tile = TMEM lane
+    const int tok_in = m_row / p.G, head_in = m_row - tok_in * p.G;
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    uint32_t tiles = 0, pairs = 0, singles[2] = {0, 0}, outs = 0;
+    bool ok = true;
+    for (uint32_t items = 0; ok; ++items) {
+      const int slot = items % ITEMS;
+      if (!warp_wait(&sm.item_full[slot], items / ITEMS, p.status)) break;
+      const Item it = sm.items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[slot]));
+      if (it.nt == 0) break;
+      const bool pair = it.half == 2;
+      if (!pair && wg == 1) {
+        tiles += it.nt;
+        continue;
+      }
+      const int tok = (pair ? wg * p.tq : 0) + tok_in;  // token of the work tile
+      const bool valid = tok_in < p.tq && tok < it.ntok;
+      const bool active = __any_sync(FULL, valid);
+      // Keys that the row sees; a row that is not stored needs no mask.
+      const int limit = !valid ? 0x7FFFFFFF : it.kvlim ? it.pos0 + tok + 1 : 0;
+      const uint32_t ocol = tl + O_COL + (pair ? wg * HD : 0);
+      float m = -INFINITY, l = 0.f;
+      for (int t = 0; t < it.nt; ++t) {
+        const int b = t & 1;
+        const int sb = pair ? wg : 2 + b;            // barrier set
+        const uint32_t scol = tl + (pair ? wg : b) * BK;
+        const uint32_t ph = pair ? pairs + t : singles[b] + (t >> 1);
+        if (!warp_wait(&sm.s_full[sb], ph, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int k0 = (it.j0 + t) * BK;
+        if (active) {
+          uint32_t v[BK];
+          tmem_ld32(scol, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_ld32(scol + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+          tmem_ld32(scol + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
+          tmem_ld32(scol + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
+          tmem_wait_ld();
+          if (__any_sync(FULL, limit < k0 + BK)) {
+#pragma unroll
+            for (int i = 0; i < BK; ++i)
+              if (k0 + i >= limit) v[i] = __float_as_uint(-INFINITY);
+          }
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx[i] = __uint_as_float(v[i]);
+#pragma unroll
+          for (int i = 8; i < BK; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(v[i]));
+          float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+          tmax *= p.scale_log2;  // the scale is positive: the maximum commutes with it
+          float factor = 1.0f;
+          bool grow = false;
+          if (t == 0) {
+            m = tmax;
+          } else if (tmax > m + 8.0f) {
+            factor = ex2(m - tmax);
+            m = tmax;
+            grow = true;
+          }
+          if (__any_sync(FULL, grow)) {
+            // Every earlier value product has to be done: a pair's score commit covers it.
+            if (!pair && !warp_wait(&sm.pv_done[b ^ 1], singles[b ^ 1] + ((t - 1) >> 1), p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            l *= factor;
+#pragma unroll 1
+            for (int x = 0; x < HD / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32(ocol + 32 * x, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+              tmem_st32(ocol + 32 * x, o);
+            }
+            tmem_wait_st();
+          }
+          // 2^(s scale - m); a row without keys so far has m = -inf and only masked scores.
+          const float mu = m == -INFINITY ? 0.f : m;
+          const float2 nm2 = make_float2(-mu, -mu), sc2 = make_float2(p.scale_log2, p.scale_log2);
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int x = 0; x < BK / 64; ++x) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              const float2 a = __ffma2_rn(
+                  make_float2(__uint_as_float(v[64 * x + i]), __uint_as_float(v[64 * x + i + 1])), sc2, nm2);
+              const float2 e = make_float2(ex2(a.x), ex2(a.y));
+              ls[(i >> 1) & 1] = __fadd2_rn(ls[(i >> 1) & 1], e);
+              pk[i / 2] = pack_bf16x2(e.x, e.y);
+            }
+            tmem_st32(scol + 32 * x, pk);
+          }
+          l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+          tmem_wait_st();  // P is in TMEM before the MMA may read it
+        }
+        if (k0 + BK > it.kvlim) {
+          // Values that no row of the tile may see: rows kvlim - k0 .. 127 of the stage.
+          const uint32_t vl = 2 * (tiles + t) + 1;
+          if (!warp_wait(&sm.ring_full[vl % STAGES], vl / STAGES, p.status)) {
+            ok = false;
+            break;
+          }
+          if (m_row >= it.kvlim - k0) {
+            uint4* z = reinterpret_cast<uint4*>(base_ptr + RING_OFF + (vl % STAGES) * TILE_BYTES + m_row * 128);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              z[x] = make_uint4(0, 0, 0, 0);
+              z[x + ATOM_BYTES / 16] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[sb]));
+      }
+      if (!ok) break;
+      tiles += it.nt;
+      if (pair) {
+        pairs += it.nt;
+      } else {
+        singles[0] += (it.nt + 1) >> 1;
+        singles[1] += it.nt >> 1;
+      }
+      // ---- the item's output: O / l, or the partial
+      if (!warp_wait(&sm.o_full[wg], outs++, p.status)) break;
+      tc_fence_after();
+      if (active) {
+        const long long trow = it.row0 + tok;
+        const int head = it.g * p.G + head_in;
+        if (it.part < 0) {
+          const float inv = 1.0f / l;
+          uint16_t* const dst = p.out + (trow * p.n_head + head) * HD;
+#pragma unroll 1
+          for (int x = 0; x < HD / 32; ++x) {
+            uint32_t o[32];
+            tmem_ld32(ocol + 32 * x, o);
+            tmem_wait_ld();
+            if (valid) {
+              uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * x);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  pk[i] = pack_bf16x2(__uint_as_float(o[8 * y + 2 * i]) * inv, __uint_as_float(o[8 * y + 2 * i + 1]) * inv);
+                d4[y] = l > 0.f ? make_uint4(pk[0], pk[1], pk[2], pk[3]) : make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
+          if (valid && p.lse) p.lse[trow * p.n_head + head] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+        } else {
+          uint8_t* const part = p.parts + (size_t)it.part * PART_BYTES;
+          const int prow = (pair ? wg * 128 : 0) + m_row;
+          float4* const po = reinterpret_cast<float4*>(part) + prow;
+#pragma unroll 1
+          for (int x = 0; x < HD / 32; ++x) {
+            uint32_t o[32];
+            tmem_ld32(ocol + 32 * x, o);
+            tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                po[(x * 8 + y) * 256] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                                                    __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+            }
+          }
+          if (valid) {
+            float* const ml = reinterpret_cast<float*>(part + PART_O);
+            ml[prow] = m;
+            ml[256 + prow] = l;
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the partials of the work tile that begins in range blockIdx.x and ends in a later one:
+// out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over its parts in the order of the keys
+// (slot 2 c + 1 of the first CTA, slots 2 c of the others).  One block per 16 rows.
+constexpr int COMBINE_ROWS = 16;
+constexpr int COMBINE_THREADS = 512;
+__global__ void __launch_bounds__(COMBINE_THREADS) paged_combine_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ float s_w[CTAS][COMBINE_ROWS];  // each part's weight per row
+  __shared__ float s_inv[COMBINE_ROWS];
   pdl_wait();
   pdl_trigger();
-  const long long w = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (w >= (long long)p.T * p.n_head) return;
-  const int t = (int)(w / p.n_head), h = (int)(w % p.n_head);
-  const int g = h / (p.n_head / p.n_kv_head);
-  int keys = 0, r = 0;
-  if (t >= p.row_start[0] && t < p.row_start[p.R]) {
-    int lo = 0, hi = p.R;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.row_start[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    r = lo;
-    const int n = p.row_start[r + 1] - p.row_start[r];
-    const int len = p.kv_len[r];
-    if (len >= n) keys = len - n + (t - p.row_start[r]) + 1;
-    if (len > (p.max_pages << p.page_shift)) {
-      keys = 0;
-      if (lane == 0) atomicOr(p.status, kDevCheck);
-    }
-  }
-  const float4 q = load4(p.q + t * p.q_stride + h * HD + lane * 4);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int page = 1 << p.page_shift;
-  for (int k = 0; k < keys; ++k) {
-    const int id = p.table[(long long)r * p.max_pages + (k >> p.page_shift)];
-    if (id < 0 || id >= p.pages) {
-      if (lane == 0) atomicOr(p.status, kDevCheck);
-      continue;
-    }
-    const long long row = ((((long long)id * p.n_kv_head + g) << p.page_shift) + (k & (page - 1))) * HD + lane * 4;
-    const float4 kk = load4(p.k + row), vv = load4(p.v + row);
-    float s = q.x * kk.x + q.y * kk.y + q.z * kk.z + q.w * kk.w;
+  const int c = blockIdx.x;
+  const Split s = p.splits[c];
+  if (s.last < 0) return;
+  const int nparts = s.last - c + 1;
+  // The rows of this block: row m of half h is token h tq + m / G, head m % G.
+  const int h = (int)blockIdx.y / (128 / COMBINE_ROWS), m0 = (int)blockIdx.y % (128 / COMBINE_ROWS) * COMBINE_ROWS;
+  const int used = min(max(s.ntok - h * p.tq, 0), p.tq) * p.G;  // rows in use of the half
+  const int rows = min(COMBINE_ROWS, used - m0);
+  if (rows <= 0) return;
+  auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * PART_BYTES; };
+  const int prow = h * 128 + m0;
+  auto row_of = [&](int r, long long& trow, int& head) {
+    const int m = m0 + r, tok = m / p.G;
+    trow = s.row0 + h * p.tq + tok;
+    head = s.g * p.G + (m - tok * p.G);
+  };
+  // One warp per row: the largest maximum, the weights, the sum.
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp < rows) {
+    float top = -INFINITY;
+    for (int i = lane; i < nparts; i += 32)
+      top = fmaxf(top, reinterpret_cast<const float*>(part(i) + PART_O)[prow + warp]);
 #pragma unroll
-    for (int b = 16; b > 0; b >>= 1) s += __shfl_xor_sync(FULL, s, b);
-    s *= p.scale;
-    const float mn = fmaxf(m, s), f = expf(m - mn), e = expf(s - mn);
-    m = mn;
-    l = l * f + e;
-    o = make_float4(o.x * f + e * vv.x, o.y * f + e * vv.y, o.z * f + e * vv.z, o.w * f + e * vv.w);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+    float sum = 0.f;
+    for (int i = lane; i < nparts; i += 32) {
+      const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
+      const float mi = ml[prow + warp];
+      const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
+      s_w[i][warp] = w;
+      sum += w * ml[256 + prow + warp];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    if (lane == 0) {
+      s_inv[warp] = sum > 0.f ? 1.0f / sum : 0.f;
+      if (p.lse) {
+        long long trow;
+        int head;
+        row_of(warp, trow, head);
+        p.lse[trow * p.n_head + head] = sum > 0.f ? (top + log2f(sum)) * LN2 : -INFINITY;
+      }
+    }
   }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  uint2 packed;
-  packed.x = *reinterpret_cast<const uint32_t*>(&a);
-  packed.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p.out + ((long long)t * p.n_head + h) * HD + lane * 4) = packed;
-  if (p.lse && lane == 0) p.lse[(long long)t * p.n_head + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  __syncthreads();
+  for (int e = threadIdx.x; e < rows * 32; e += COMBINE_THREADS) {
+    const int r = e % rows, c4 = e / rows;  // neighbouring threads, neighbouring rows
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < nparts; ++i) {
+      const float w = s_w[i][r];
+      if (w != 0.f) {
+        const float4 x = reinterpret_cast<const float4*>(part(i))[c4 * 256 + prow + r];
+        o = make_float4(o.x + w * x.x, o.y + w * x.y, o.z + w * x.z, o.w + w * x.w);
+      }
+    }
+    const float inv = s_inv[r];
+    long long trow;
+    int head;
+    row_of(r, trow, head);
+    reinterpret_cast<uint2*>(p.out + (trow * p.n_head + head) * HD)[c4] =
+        inv > 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+  }
 }
 
 }  // namespace
 
-size_t paged_attention_scratch_bytes(const moe_paged_shape_t&) { return 16; }
+size_t paged_attention_scratch_bytes(const moe_paged_shape_t&) { return SCRATCH_BYTES; }
 
 cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q, long long q_stride,
                                    const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* block_table,
-                                   const int32_t* row_start, const int32_t* kv_len, uint16_t* out, float* lse, void*,
-                                   cudaStream_t st) {
-  int shift = 0;
-  while ((1 << shift) < s.page_size) ++shift;
-  PagedParams p{q, k_cache, v_cache, block_table, row_start, kv_len, out, lse, device_status_ptr(), q_stride,
-                s.requests, s.tokens, s.n_head, s.n_kv_head, s.pages, s.max_pages, shift, 1.0f / sqrtf((float)HD)};
+                                   const int32_t* row_start, const int32_t* kv_len, uint16_t* out, float* lse,
+                                   void* scratch, cudaStream_t st) {
+  PagedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.G = s.n_head / s.n_kv_head;
+  p.tq = 128;
+  while (p.tq * p.G > 128) p.tq >>= 1;  // 128 / (G rounded up to a power of two)
+  while ((1 << p.page_shift) < s.page_size) ++p.page_shift;
+  const uint64_t qdims[4] = {64, 2, (uint64_t)s.n_head, (uint64_t)s.tokens};
+  const uint64_t qstrides[3] = {128, 256, (uint64_t)q_stride * 2};
+  const uint32_t qbox[4] = {64, 1, (uint32_t)p.G, (uint32_t)p.tq};
+  const uint64_t rows = (uint64_t)s.pages * s.n_kv_head * s.page_size;
+  const uint64_t kdims[3] = {64, rows, 2}, kstrides[2] = {256, 128};
+  const uint32_t kbox[3] = {64, (uint32_t)s.page_size, 1};
+  if (!encode_tma_bf16(&p.q, q, 4, qdims, qstrides, qbox) || !encode_tma_bf16(&p.k, k_cache, 3, kdims, kstrides, kbox) ||
+      !encode_tma_bf16(&p.v, v_cache, 3, kdims, kstrides, kbox))
+    return cudaErrorInvalidValue;
+  p.table = block_table;
+  p.row_start = row_start;
+  p.kv_len = kv_len;
+  p.out = out;
+  p.lse = lse;
+  p.splits = static_cast<Split*>(scratch);
+  p.parts = static_cast<uint8_t*>(scratch) + CTAS * sizeof(Split);
+  p.status = device_status_ptr();
   if (!p.status) return cudaErrorInvalidDevicePointer;
-  const long long warps = (long long)s.tokens * s.n_head;
-  return launch_pdl(paged_attention_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, p);
+  p.R = s.requests;
+  p.T = s.tokens;
+  p.n_head = s.n_head;
+  p.n_kv_head = s.n_kv_head;
+  p.pages = s.pages;
+  p.max_pages = s.max_pages;
+  p.scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
+  cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess) e = launch_pdl(paged_attention_kernel, dim3(CTAS), dim3(THREADS), SMEM_BYTES, st, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(paged_combine_kernel, dim3(CTAS, 2 * 128 / COMBINE_ROWS), dim3(COMBINE_THREADS), 0, st, p);
+  return e;
 }
 
 }  // namespace moe
