@@ -15,23 +15,26 @@
 //
 // Work.  The unit is one 128-key tile of one work tile.  All units of the call, in order
 // (request, key/value head, query tile, key tile), are split into equal contiguous ranges, one
-// per CTA, whatever the requests' lengths: a range holds the end of one work tile, whole work
+// per CTA, whatever the requests' lengths (a work tile counts one unit more than it has key
+// tiles, for its query load and its output): a range holds the end of one work tile, whole work
 // tiles and the beginning of another.  A work tile that does not lie in one range leaves
 // partial outputs, which paged_combine_kernel joins in the order of the keys.  Every CTA
 // computes the ranges itself from the lengths (one prefix sum over the requests), so the call
 // needs no plan, no counters and no cleared workspace.  Rows that belong to no request are the
 // rows of one more request without keys; their units read nothing and give zeros.
 //
-// paged_attention_kernel, one CTA per SM, 10 warps:
-//   - warp 8 walks the CTA's range, publishes each item (work tile, key tiles) in a small
+// paged_attention_kernel, one CTA per SM, 18 warps:
+//   - warp 16 walks the CTA's range, publishes each item (work tile, key tiles) in a small
 //     ring, and issues the TMA copies: the query halves, and one box per page and 64-column
 //     half of the key and value tiles, into a ring of five 32 KB stages;
-//   - warp 9 (one thread) issues tcgen05.mma: S = Q K^T into a score buffer, O += P V with P
+//   - warp 17 (one thread) issues tcgen05.mma: S = Q K^T into a score buffer, O += P V with P
 //     (bf16) read from the score buffer's own columns.  The pipe runs in order, so a score
 //     product that overwrites a buffer needs no wait for the product that read P from it;
-//   - warps 0-3 and 4-7 (one query row per thread, its TMEM lane): the online softmax in the
-//     log2 domain on 128 scores held in registers, O rescaled only when the row's maximum
-//     grew by more than 8 (2^8); at the end O / l, or O, m and l as a partial.
+//   - warps 0-7 and 8-15, a warp per 16 rows: the online softmax in the log2 domain.  TMEM is
+//     read in the 16 x 256-bit shape, four lanes per row with 32 scores each, so that two
+//     warps per SM sub-partition share a half tile and the row maximum is two shuffles; O is
+//     rescaled only when a row's maximum grew by more than 8 (2^8); at the end O / l, or O, m
+//     and l as a partial.
 // Values past the last key that a tile may see are zeroed in shared memory before P V: their
 // weight is 0, but 0 times a stale NaN or infinity is not.
 // Every barrier wait is bounded; on a timeout the status word is set and the CTA exits.
@@ -52,8 +55,11 @@ constexpr int ATOM_BYTES = 128 * 64 * 2;      // 16 KB: 128 rows x 64 bf16, 128-
 constexpr int TILE_BYTES = 2 * ATOM_BYTES;    // 32 KB: 128 rows x 128
 constexpr int STAGES = 5;                     // key and value tiles in flight: K0 V0 K1 V1 ...
 constexpr int RING_OFF = 2 * TILE_BYTES;      // after the two query halves
-constexpr int SMEM_BYTES = RING_OFF + STAGES * TILE_BYTES + 1024;
-constexpr int THREADS = 320;
+constexpr int STATE_OFF = RING_OFF + STAGES * TILE_BYTES;
+constexpr int SMEM_BYTES = STATE_OFF + 1024;
+constexpr int SOFTMAX_WARPS = 16;             // eight per query half, 16 rows each
+constexpr int LOAD_WARP = 16, MMA_WARP = 17;
+constexpr int THREADS = 576;
 constexpr int WARPS = THREADS / 32;
 constexpr int ITEMS = 4;                      // depth of the item ring
 constexpr int CTAS = 152;                     // one per SM
@@ -63,9 +69,9 @@ constexpr unsigned FULL = 0xFFFFFFFFu;
 constexpr float LN2 = 0.6931471805599453f;
 
 // Partials: per CTA two slots (a work tile continued from the range before; one that goes on in
-// the next range), each O [32][256] float4 (columns by four, then rows: coalesced over the
-// rows) and m, l [256].
-constexpr size_t PART_O = 32 * 256 * 16;
+// the next range), each O [16][256][8] fp32 (groups of eight columns, rows: what a warp stores
+// at once is contiguous) and m, l [256].
+constexpr size_t PART_O = 16 * 256 * 32;
 constexpr size_t PART_BYTES = PART_O + 2 * 256 * 4;
 
 // One work tile that goes on past the range of the CTA that begins it.
@@ -86,7 +92,7 @@ struct PagedParams {
   Split* splits;
   uint8_t* parts;
   int* status;
-  int R, T, n_head, n_kv_head, G, tq, pages, max_pages, page_shift;
+  int R, T, n_head, n_kv_head, G, tq, tQ_shift, pages, max_pages, page_shift;
   float scale_log2;  // log2(e) / sqrt(HD)
 };
 
@@ -106,7 +112,10 @@ struct Request {
   int qn;             // work tiles per key/value head
 };
 
-__device__ __forceinline__ long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+// a / b, in 32 bits where both fit (a 64-bit division is a subroutine).
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // Request r; r == R is the padding rows.  Lengths out of range are reported once per call
 // (`report`) and leave a request without keys or without rows.
@@ -121,32 +130,33 @@ __device__ Request load_request(const PagedParams& p, int r, bool report) {
   q.n = rows_ok ? b - a : 0;
   q.dead = !kv_ok || kv < q.n || r == p.R;
   q.ctx = q.dead ? 0 : kv - q.n;
-  const int tQ = 2 * p.tq;
-  q.qn = (q.n + tQ - 1) / tQ;
+  q.qn = (q.n + (1 << p.tQ_shift) - 1) >> p.tQ_shift;
   return q;
 }
 
-// Units of the request's first k work tiles, all full (2 tq tokens): tile i reaches position
-// ctx + (i + 1) 2 tq.  With 2 tq dividing 128, ceil((ctx + (i + 1) tQ) / 128) =
-// ceil((c0 + i + 1) / P) for c0 = ceil(ctx / tQ) and P = 128 / tQ, and the sum over i is a
-// difference of sums of ceil(m / P); with 2 tq = 256 a tile adds two key tiles to the last.
-__device__ long long units_of_full(const Request& q, long long k, int tQ) {
-  if (q.dead) return k;
-  if (tQ > BK) return k * (k + 1) + k * cdiv(q.ctx, BK);
-  const long long P = BK / tQ, c0 = cdiv(q.ctx, tQ);
-  auto sum = [P](long long n) {
-    const long long d = n / P, rem = n - d * P;
-    return P * (d * (d + 1) / 2) + rem * (d + 1);
+// Key tiles of the request's first k work tiles, all full (tQ = 2 tq tokens), and one unit
+// for each: tile i reaches position ctx + (i + 1) tQ.  With tQ dividing 128,
+// ceil((ctx + (i + 1) tQ) / 128) = ceil((c0 + i + 1) / P) for c0 = ceil(ctx / tQ) and
+// P = 128 / tQ, and the sum over i is a difference of sums of ceil(m / P); with tQ = 256 a
+// tile adds two key tiles to the last.
+__device__ __forceinline__ long long units_of_full(const Request& q, long long k, int tQ_shift) {
+  if (q.dead) return 2 * k;
+  if (tQ_shift > 7) return k * (k + 1) + k * ((q.ctx + BK - 1) >> 7) + k;
+  const int ps = 7 - tQ_shift;
+  const long long c0 = (q.ctx + (1 << tQ_shift) - 1) >> tQ_shift;
+  auto sum = [ps](long long n) {
+    const long long d = n >> ps, rem = n & ((1 << ps) - 1);
+    return ((d * (d + 1)) >> 1 << ps) + rem * (d + 1);
   };
-  return sum(c0 + k) - sum(c0);
+  return sum(c0 + k) - sum(c0) + k;
 }
-__device__ __forceinline__ int tile_units(const Request& q, int i, int tQ) {
-  return q.dead ? 1 : (int)cdiv(q.ctx + min(q.n, (i + 1) * tQ), BK);
+__device__ __forceinline__ int key_tiles(const Request& q, int i, int tQ_shift) {
+  return q.dead ? 1 : (q.ctx + min(q.n, (i + 1) << tQ_shift) + BK - 1) >> 7;
 }
 // Units of one key/value head of the request.
-__device__ long long head_units(const Request& q, int tQ) {
+__device__ __forceinline__ long long head_units(const Request& q, int tQ_shift) {
   if (q.qn == 0) return 0;
-  return units_of_full(q, q.qn - 1, tQ) + tile_units(q, q.qn - 1, tQ);
+  return units_of_full(q, q.qn - 1, tQ_shift) + key_tiles(q, q.qn - 1, tQ_shift) + 1;
 }
 
 struct SmemState {
@@ -163,6 +173,7 @@ struct SmemState {
   int start_req;
   uint32_t tmem;
 };
+static_assert(sizeof(SmemState) <= SMEM_BYTES - STATE_OFF, "the state fits behind the ring");
 
 // Warp-wide wait by lane 0.
 __device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, int* status) {
@@ -178,15 +189,69 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) SmemState sm;
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int tQ = 2 * p.tq;
+// TMEM in the 16 x 256-bit shape: sixteen rows, `n` groups of eight fp32 columns; a lane holds
+// columns 2 (lane % 4) + {0, 1} of every group of rows lane / 4 (registers 4 g, 4 g + 1) and
+// lane / 4 + 8 (4 g + 2, 4 g + 3).
+__device__ __forceinline__ void tmem_ld_quad8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_quad4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_quad4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// The 16 x 128-bit shape, eight groups of four 32-bit columns: column lane % 4 of every group of
+// rows lane / 4 (register 2 g) and lane / 4 + 8 (2 g + 1): the bf16 pairs of the shape above.
+__device__ __forceinline__ void tmem_st_pairs8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 
-  if (warp == 8 && lane == 0) {
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(FULL, x, 1));
+  return fmaxf(x, __shfl_xor_sync(FULL, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(FULL, x, 1);
+  return x + __shfl_xor_sync(FULL, x, 2);
+}
+
+__global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  SmemState& sm = *reinterpret_cast<SmemState*>(smem + STATE_OFF);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (base & 1023u) {  // the swizzled tiles need it; the declaration asks for it
+    if (tid == 0) atomicOr(p.status, kDevCheck);
+    return;
+  }
+
+  if (warp == LOAD_WARP && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.q_full[i]), 1);
       mbar_init(smem_u32(&sm.q_empty[i]), 1);
@@ -199,18 +264,18 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.p_full[i]), SOFTMAX_WARPS / 2);
     }
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(smem_u32(&sm.item_full[i]), 1);
-      mbar_init(smem_u32(&sm.item_empty[i]), 9);  // the issuer and eight softmax warps
+      mbar_init(smem_u32(&sm.item_empty[i]), 1 + SOFTMAX_WARPS);  // the issuer and the softmax warps
     }
     fence_mbar_init();
     tma_prefetch_desc(&p.q);
     tma_prefetch_desc(&p.k);
     tma_prefetch_desc(&p.v);
   }
-  if (warp == 9) {
+  if (warp == MMA_WARP) {
     tmem_alloc(smem_u32(&sm.tmem), TMEM_COLS);
     tmem_relinquish();
   }
@@ -222,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   const int per = (nreq + THREADS - 1) / THREADS;
   const int r0 = min(nreq, tid * per), r1 = min(nreq, r0 + per);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += head_units(load_request(p, r, blockIdx.x == 0), tQ) * p.n_kv_head;
+  for (int r = r0; r < r1; ++r) mine += head_units(load_request(p, r, blockIdx.x == 0), p.tQ_shift) * p.n_kv_head;
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -242,11 +307,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   const int ctas = (int)min((long long)gridDim.x, total);  // every range holds a unit
   const int c = blockIdx.x;
   const bool working = c < ctas;
-  const long long u0 = working ? total * c / ctas : 0, u1 = working ? total * (c + 1) / ctas : 0;
+  const long long u0 = working ? div_ll(total * c, ctas) : 0, u1 = working ? div_ll(total * (c + 1), ctas) : 0;
   if (working && mine > 0 && u0 >= upto - mine && u0 < upto) {
     long long at = upto - mine;
     for (int r = r0; r < r1; ++r) {
-      const long long w = head_units(load_request(p, r, false), tQ) * p.n_kv_head;
+      const long long w = head_units(load_request(p, r, false), p.tQ_shift) * p.n_kv_head;
       if (u0 < at + w) {
         sm.start_req = r;
         sm.start_off = u0 - at;
@@ -260,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   const uint32_t tmem = sm.tmem;
 
   if (!working) {
-  } else if (warp == 8) {
+  } else if (warp == LOAD_WARP) {
     // ------------------------------------------------------------ walk and TMA copies
     const int nb = BK >> p.page_shift;         // pages per key tile
     const int box = lane & (nb - 1), col = lane >= nb ? 1 : 0;
@@ -270,108 +335,109 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     const int rows_end = (int)((long long)p.pages * p.n_kv_head << p.page_shift);  // out of range: zeros
     int r = sm.start_req;
     Request q = load_request(p, r, false);
-    long long w = head_units(q, tQ);
-    int g = (int)(sm.start_off / w);
+    const long long w = head_units(q, p.tQ_shift);
+    int g = (int)div_ll(sm.start_off, w);
     const long long off = sm.start_off - g * w;
     int i = 0;  // the work tile that holds unit `off` of the head: units_of_full(i) <= off
     {
       int hi = q.qn;
       while (hi - i > 1) {
         const int mid = (i + hi) >> 1;
-        if (units_of_full(q, mid, tQ) <= off) i = mid;
+        if (units_of_full(q, mid, p.tQ_shift) <= off) i = mid;
         else hi = mid;
       }
     }
-    int j = (int)(off - units_of_full(q, i, tQ));
-    long long left = u1 - u0, unit = u0;
+    int j = (int)(off - units_of_full(q, i, p.tQ_shift));
+    long long unit = u0;
     uint32_t items = 0, loads = 0, q_uses[2] = {0, 0};
     int next_half = 0;
     bool ok = true;
-    while (ok) {
+    while (ok && unit < u1) {
+      const int tile_n = key_tiles(q, i, p.tQ_shift);
+      const int units = (int)min((long long)(tile_n + 1 - j), u1 - unit);  // of this work tile in the range
       Item it;
-      it.nt = 0;
-      int tile_n = 0;
-      if (left > 0) {
-        tile_n = tile_units(q, i, tQ);
-        it.row0 = q.row0 + i * tQ;
-        it.ntok = min(tQ, q.n - i * tQ);
-        it.pos0 = q.ctx + i * tQ;
-        it.kvlim = q.dead ? 0 : it.pos0 + it.ntok;
-        it.j0 = j;
-        it.nt = (int)min((long long)(tile_n - j), left);
-        it.g = g;
+      it.row0 = q.row0 + (i << p.tQ_shift);
+      it.ntok = min(1 << p.tQ_shift, q.n - (i << p.tQ_shift));
+      it.pos0 = q.ctx + (i << p.tQ_shift);
+      it.kvlim = q.dead ? 0 : it.pos0 + it.ntok;
+      it.j0 = j;
+      it.nt = min(units, tile_n - j);  // the unit past the key tiles holds no work
+      it.g = g;
+      if (it.nt > 0) {
+        // Page ids of the first key tile, on their way while the item is published.
+        const int32_t* const row = p.table + (long long)r * p.max_pages;
+        auto page_id = [&](int t) {  // -1: no key there that the tile may see
+          const int page = (it.j0 + t) * nb + box;
+          return copies && ((long long)page << p.page_shift) < it.kvlim ? row[page] : -1;
+        };
+        int id = page_id(0);
         it.half = it.ntok > p.tq ? 2 : next_half;
         const bool ends = j + it.nt == tile_n;
         it.part = j == 0 && ends ? -1 : (j == 0 ? 2 * c + 1 : 2 * c);
+        const int slot = items % ITEMS;
+        if (!warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status)) break;
+        if (lane == 0) {
+          sm.items[slot] = it;
+          mbar_arrive(smem_u32(&sm.item_full[slot]));
+        }
+        __syncwarp();
+        ++items;
+        // The key and value tiles, one box per page and column half and lane; the query
+        // halves behind the first key tile.
+        for (int t = 0; t < it.nt && ok; ++t) {
+          const bool there = ((long long)((it.j0 + t) * nb + box) << p.page_shift) < it.kvlim;
+          int coord = rows_end;
+          if (copies && there) {
+            if (id >= 0 && id < p.pages) coord = (id * p.n_kv_head + g) << p.page_shift;
+            else atomicOr(p.status, kDevCheck);
+          }
+          if (t + 1 < it.nt) id = page_id(t + 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = loads % STAGES;
+            if (!warp_wait(&sm.ring_empty[st], (loads / STAGES) ^ 1u, p.status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t bar = smem_u32(&sm.ring_full[st]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, TILE_BYTES);
+            __syncwarp();
+            if (copies)
+              tma_load_3d(base + RING_OFF + st * TILE_BYTES + box_dst, kv ? &p.v : &p.k, bar, 0, coord, col);
+            ++loads;
+            if (t == 0 && kv == 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (!ok || (it.half != 2 && it.half != h)) continue;
+                ok = warp_wait(&sm.q_empty[h], q_uses[h] ^ 1u, p.status);
+                if (!ok) continue;
+                if (lane == 0) {
+                  const uint32_t qbar = smem_u32(&sm.q_full[h]);
+                  mbar_arrive_expect_tx(qbar, q_bytes);
+                  const int tok = it.row0 + (it.half == 2 ? h * p.tq : 0);
+                  tma_load_4d(base + h * TILE_BYTES, &p.q, qbar, 0, 0, g * p.G, tok);
+                  tma_load_4d(base + h * TILE_BYTES + ATOM_BYTES, &p.q, qbar, 0, 1, g * p.G, tok);
+                }
+                ++q_uses[h];
+              }
+              if (!ok) break;
+            }
+          }
+        }
+        if (it.half != 2) next_half = it.half ^ 1;
         if (j == 0 && !ends && lane == 0) {
-          // The unit after the tile's last one belongs to CTA ((u + 1) ctas - 1) / total.
-          const long long end = unit + tile_n;
+          // The unit after the tile's last key tile belongs to CTA ((u + 1) ctas - 1) / total.
           Split s;
           s.row0 = it.row0;
           s.ntok = it.ntok;
           s.g = g;
-          s.last = (int)((end * ctas - 1) / total);
+          s.last = (int)div_ll((unit + tile_n) * ctas - 1, total);
           p.splits[c] = s;
         }
       }
-      const int slot = items % ITEMS;
-      if (!warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status)) break;
-      if (lane == 0) {
-        sm.items[slot] = it;
-        mbar_arrive(smem_u32(&sm.item_full[slot]));
-      }
-      __syncwarp();
-      ++items;
-      if (it.nt == 0) break;
-
-      // The query halves.
-      for (int h = 0; h < 2; ++h) {
-        if (it.half != 2 && it.half != h) continue;
-        if (!warp_wait(&sm.q_empty[h], q_uses[h] ^ 1u, p.status)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sm.q_full[h]);
-          mbar_arrive_expect_tx(bar, q_bytes);
-          const int tok = it.row0 + (it.half == 2 ? h * p.tq : 0);
-          tma_load_4d(base + h * TILE_BYTES, &p.q, bar, 0, 0, g * p.G, tok);
-          tma_load_4d(base + h * TILE_BYTES + ATOM_BYTES, &p.q, bar, 0, 1, g * p.G, tok);
-        }
-        ++q_uses[h];
-      }
-      if (!ok) break;
-      if (it.half != 2) next_half = it.half ^ 1;
-
-      // The key and value tiles, one box per page and column half and lane.
-      const int32_t* const row = p.table + (long long)r * p.max_pages;
-      for (int t = 0; t < it.nt && ok; ++t) {
-        const int page = (it.j0 + t) * nb + box;
-        int coord = rows_end;
-        if (copies && ((long long)page << p.page_shift) < it.kvlim) {
-          const int id = row[page];
-          if (id >= 0 && id < p.pages) coord = (id * p.n_kv_head + g) << p.page_shift;
-          else atomicOr(p.status, kDevCheck);
-        }
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int st = loads % STAGES;
-          if (!warp_wait(&sm.ring_empty[st], (loads / STAGES) ^ 1u, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = smem_u32(&sm.ring_full[st]);
-          if (lane == 0) mbar_arrive_expect_tx(bar, TILE_BYTES);
-          __syncwarp();
-          if (copies)
-            tma_load_3d(base + RING_OFF + st * TILE_BYTES + box_dst, kv ? &p.v : &p.k, bar, 0, coord, col);
-          ++loads;
-        }
-      }
-      left -= it.nt;
-      unit += it.nt;
+      unit += units;
       // The next work tile: query tile, then head, then request.
-      if (left > 0) {
+      if (unit < u1) {
         j = 0;
         if (++i == q.qn) {
           i = 0;
@@ -383,17 +449,25 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         }
       }
     }
+    if (ok) {  // nt == 0 ends the walk
+      const int slot = items % ITEMS;
+      if (warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status) && lane == 0) {
+        sm.items[slot].nt = 0;
+        mbar_arrive(smem_u32(&sm.item_full[slot]));
+      }
+      __syncwarp();
+    }
     // No copy may still be landing when the CTA exits.
     for (int h = 0; h < 2; ++h)
       if (q_uses[h]) warp_wait(&sm.q_full[h], q_uses[h] - 1, p.status);
     for (uint32_t l = loads > STAGES ? loads - STAGES : 0; l < loads; ++l)
       warp_wait(&sm.ring_full[l % STAGES], l / STAGES, p.status);
-  } else if (warp == 9) {
+  } else if (warp == MMA_WARP) {
     if (lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16_f32(128, BK, 0, 0);
       constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, 0, 1);
-      uint32_t q_uses[2] = {0, 0}, tiles = 0, pairs = 0, singles[2] = {0, 0};
+      uint32_t q_uses[2] = {0, 0}, tiles = 0, pairs = 0, even = 0, odd = 0;
       auto wait = [&](const uint64_t* bar, uint32_t parity) {
         return mbar_wait_spin(smem_u32(bar), parity & 1u, p.status);
       };
@@ -409,8 +483,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         const uint64_t vd = sw128_mnmajor_desc(base + RING_OFF + st * TILE_BYTES, ATOM_BYTES);
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          tc_mma_bf16_a_tmem(tmem + O_COL + out * HD, tmem + buf * BK + kk * 8, vd + kk * 128u, id_pv,
-                             !first || kk != 0);
+          tc_mma_bf16_a_tmem(tmem + O_COL + out * HD, tmem + buf * BK + (kk >> 2) * 64 + (kk & 3) * 8,
+                             vd + kk * 128u, id_pv, !first || kk != 0);
       };
       for (uint32_t items = 0;; ++items) {
         const int slot = items % ITEMS;
@@ -420,8 +494,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (nt == 0) break;
         const bool pair = half == 2;
         bool ok = true;
-        for (int h = 0; h < 2 && ok; ++h)
-          if (pair || half == h) ok = wait(&sm.q_full[h], q_uses[h]++);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (ok && (pair || half == h)) ok = wait(&sm.q_full[h], q_uses[h]++);
         // Key tile t of the item is load 2 (tiles + t), its value tile the next one.
         auto ready = [&](int t, int kv) {
           const uint32_t l = 2 * (tiles + t) + kv;
@@ -480,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               tc_commit(smem_u32(&sm.ring_empty[stage(t + 1, 0)]));
             }
             if (t + 1 == nt) tc_commit(smem_u32(&sm.q_empty[half]));  // every score product is issued
-            if (!wait(&sm.p_full[2 + b], singles[b] + (t >> 1)) || !ready(t, 1)) {
+            if (!wait(&sm.p_full[2 + b], (b ? odd : even) + (t >> 1)) || !ready(t, 1)) {
               ok = false;
               break;
             }
@@ -490,8 +565,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             tc_commit(smem_u32(&sm.pv_done[b]));
             if (t + 1 == nt) tc_commit(smem_u32(&sm.o_full[0]));
           }
-          singles[0] += (nt + 1) >> 1;
-          singles[1] += nt >> 1;
+          even += (nt + 1) >> 1;
+          odd += nt >> 1;
         }
         if (!ok) break;
         tiles += nt;
@@ -499,124 +574,158 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     }
   } else {
     // ------------------------------------------------------------ softmax warps
-    const int wg = warp >> 2, q4 = warp & 3;
-    const int m_row = q4 * 32 + lane;              // row of the half tile = TMEM lane
-    const int tok_in = m_row / p.G, head_in = m_row - tok_in * p.G;
-    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-    uint32_t tiles = 0, pairs = 0, singles[2] = {0, 0}, outs = 0;
+    const int wg = warp >> 3;
+    const int lane0 = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;  // the warp's sixteen rows of the half
+    const int quad = lane & 3;
+    const uint32_t tl = tmem + ((uint32_t)lane0 << 16);
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    uint32_t tiles = 0, pairs = 0, even = 0, odd = 0, outs = 0;  // even, odd: a single item's key tiles
     bool ok = true;
     for (uint32_t items = 0; ok; ++items) {
       const int slot = items % ITEMS;
       if (!warp_wait(&sm.item_full[slot], items / ITEMS, p.status)) break;
-      const Item it = sm.items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[slot]));
-      if (it.nt == 0) break;
+      const Item& it = sm.items[slot];  // this warp's until it arrives at item_empty
+      const int nt = it.nt;
       const bool pair = it.half == 2;
-      if (!pair && wg == 1) {
-        tiles += it.nt;
+      if (nt == 0 || (!pair && wg == 1)) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[slot]));
+        if (nt == 0) break;
+        tiles += nt;
         continue;
       }
-      const int tok = (pair ? wg * p.tq : 0) + tok_in;  // token of the work tile
-      const bool valid = tok_in < p.tq && tok < it.ntok;
-      const bool active = __any_sync(FULL, valid);
-      // Keys that the row sees; a row that is not stored needs no mask.
-      const int limit = !valid ? 0x7FFFFFFF : it.kvlim ? it.pos0 + tok + 1 : 0;
+      const int kvlim = it.kvlim, first_key = it.j0 * BK;
+      // Keys that this lane's rows (lane0 + lane / 4 and eight further) see; a row that is not
+      // stored needs no mask.
+      int limit[2];
+      uint32_t valid = 0;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int tok_in = (lane0 + lane / 4 + 8 * x) / p.G, tok = (pair ? wg * p.tq : 0) + tok_in;
+        const bool v = tok_in < p.tq && tok < it.ntok;
+        limit[x] = !v ? 0x7FFFFFFF : kvlim ? it.pos0 + tok + 1 : 0;
+        valid |= v ? 1u << x : 0u;
+      }
+      const bool active = __any_sync(FULL, valid != 0);
       const uint32_t ocol = tl + O_COL + (pair ? wg * HD : 0);
-      float m = -INFINITY, l = 0.f;
-      for (int t = 0; t < it.nt; ++t) {
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int t = 0; t < nt; ++t) {
         const int b = t & 1;
         const int sb = pair ? wg : 2 + b;            // barrier set
         const uint32_t scol = tl + (pair ? wg : b) * BK;
-        const uint32_t ph = pair ? pairs + t : singles[b] + (t >> 1);
+        const uint32_t ph = pair ? pairs + t : (b ? odd : even) + (t >> 1);
         if (!warp_wait(&sm.s_full[sb], ph, p.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int k0 = (it.j0 + t) * BK;
+        const int k0 = first_key + t * BK;
         if (active) {
-          uint32_t v[BK];
-          tmem_ld32(scol, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-          tmem_ld32(scol + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-          tmem_ld32(scol + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
-          tmem_ld32(scol + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
-          tmem_wait_ld();
-          if (__any_sync(FULL, limit < k0 + BK)) {
+          // Two halves of 64 keys.  The maximum needs both; the first is read again for its
+          // exponentials, so that one half is in registers at a time (96 a thread: 16 warps).
+          const bool edge = __any_sync(FULL, min(limit[0], limit[1]) < k0 + BK);
+          uint32_t v[32];
+          auto mask = [&](int y) {
+            if (edge) {
 #pragma unroll
-            for (int i = 0; i < BK; ++i)
-              if (k0 + i >= limit) v[i] = __float_as_uint(-INFINITY);
+              for (int i = 0; i < 32; ++i)
+                if (k0 + 64 * y + (i >> 2) * 8 + quad * 2 + (i & 1) >= limit[(i >> 1) & 1])
+                  v[i] = __float_as_uint(-INFINITY);
+            }
+          };
+          float tmax[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            tmem_ld_quad8(scol + 64 * y, v);
+            tmem_wait_ld();
+            mask(y);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float mx[2];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float a = fmaxf(__uint_as_float(v[4 * i + 2 * x]), __uint_as_float(v[4 * i + 2 * x + 1]));
+                mx[i & 1] = i < 2 ? a : fmaxf(mx[i & 1], a);
+              }
+              const float a = fmaxf(mx[0], mx[1]);
+              tmax[x] = y ? fmaxf(tmax[x], a) : a;
+            }
           }
-          float mx[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = __uint_as_float(v[i]);
-#pragma unroll
-          for (int i = 8; i < BK; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(v[i]));
-          float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-          tmax *= p.scale_log2;  // the scale is positive: the maximum commutes with it
-          float factor = 1.0f;
+          // The scale is positive: the maximum commutes with it.
+          tmax[0] = quad_max(tmax[0]) * p.scale_log2;
+          tmax[1] = quad_max(tmax[1]) * p.scale_log2;
+          float factor[2] = {1.0f, 1.0f};
           bool grow = false;
-          if (t == 0) {
-            m = tmax;
-          } else if (tmax > m + 8.0f) {
-            factor = ex2(m - tmax);
-            m = tmax;
-            grow = true;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (t == 0) {
+              m[x] = tmax[x];
+            } else if (tmax[x] > m[x] + 8.0f) {
+              factor[x] = ex2(m[x] - tmax[x]);
+              m[x] = tmax[x];
+              grow = true;
+            }
           }
           if (__any_sync(FULL, grow)) {
             // Every earlier value product has to be done: a pair's score commit covers it.
-            if (!pair && !warp_wait(&sm.pv_done[b ^ 1], singles[b ^ 1] + ((t - 1) >> 1), p.status)) {
+            if (!pair && !warp_wait(&sm.pv_done[b ^ 1], (b ? even : odd) + ((t - 1) >> 1), p.status)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            l *= factor;
+            l[0] *= factor[0];
+            l[1] *= factor[1];
 #pragma unroll 1
             for (int x = 0; x < HD / 32; ++x) {
-              uint32_t o[32];
-              tmem_ld32(ocol + 32 * x, o);
+              uint32_t o[16];
+              tmem_ld_quad4(ocol + 32 * x, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-              tmem_st32(ocol + 32 * x, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor[(i >> 1) & 1]);
+              tmem_st_quad4(ocol + 32 * x, o);
             }
             tmem_wait_st();
           }
           // 2^(s scale - m); a row without keys so far has m = -inf and only masked scores.
-          const float mu = m == -INFINITY ? 0.f : m;
-          const float2 nm2 = make_float2(-mu, -mu), sc2 = make_float2(p.scale_log2, p.scale_log2);
+          const float mu0 = m[0] == -INFINITY ? 0.f : -m[0], mu1 = m[1] == -INFINITY ? 0.f : -m[1];
           float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int x = 0; x < BK / 64; ++x) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const float2 a = __ffma2_rn(
-                  make_float2(__uint_as_float(v[64 * x + i]), __uint_as_float(v[64 * x + i + 1])), sc2, nm2);
-              const float2 e = make_float2(ex2(a.x), ex2(a.y));
-              ls[(i >> 1) & 1] = __fadd2_rn(ls[(i >> 1) & 1], e);
-              pk[i / 2] = pack_bf16x2(e.x, e.y);
+          for (int y = 1; y >= 0; --y) {
+            if (y == 0) {
+              tmem_ld_quad8(scol, v);
+              tmem_wait_ld();
+              mask(0);
             }
-            tmem_st32(scol + 32 * x, pk);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int x = i & 1;
+              const float mu = x ? mu1 : mu0;
+              const float2 a = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2,
+                                          make_float2(mu, mu));
+              const float2 e = make_float2(ex2(a.x), ex2(a.y));
+              ls[x] = __fadd2_rn(ls[x], e);
+              pk[i] = pack_bf16x2(e.x, e.y);
+            }
+            tmem_st_pairs8(scol + 64 * y, pk);  // over the half's own scores
           }
-          l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+          l[0] += ls[0].x + ls[0].y;
+          l[1] += ls[1].x + ls[1].y;
           tmem_wait_st();  // P is in TMEM before the MMA may read it
         }
-        if (k0 + BK > it.kvlim) {
+        if (k0 + BK > kvlim) {
           // Values that no row of the tile may see: rows kvlim - k0 .. 127 of the stage.
           const uint32_t vl = 2 * (tiles + t) + 1;
           if (!warp_wait(&sm.ring_full[vl % STAGES], vl / STAGES, p.status)) {
             ok = false;
             break;
           }
-          if (m_row >= it.kvlim - k0) {
-            uint4* z = reinterpret_cast<uint4*>(base_ptr + RING_OFF + (vl % STAGES) * TILE_BYTES + m_row * 128);
+          const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
+          if (zrow >= kvlim - k0) {
+            uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + zcol * ATOM_BYTES +
+                                                      zrow * 128);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              z[x] = make_uint4(0, 0, 0, 0);
-              z[x + ATOM_BYTES / 16] = make_uint4(0, 0, 0, 0);
-            }
+            for (int x = 0; x < 8; ++x) z[x] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
           }
         }
@@ -625,69 +734,93 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[sb]));
       }
       if (!ok) break;
-      tiles += it.nt;
+      tiles += nt;
       if (pair) {
-        pairs += it.nt;
+        pairs += nt;
       } else {
-        singles[0] += (it.nt + 1) >> 1;
-        singles[1] += it.nt >> 1;
+        even += (nt + 1) >> 1;
+        odd += nt >> 1;
       }
       // ---- the item's output: O / l, or the partial
+      l[0] = quad_sum(l[0]);
+      l[1] = quad_sum(l[1]);
       if (!warp_wait(&sm.o_full[wg], outs++, p.status)) break;
       tc_fence_after();
       if (active) {
-        const long long trow = it.row0 + tok;
-        const int head = it.g * p.G + head_in;
         if (it.part < 0) {
-          const float inv = 1.0f / l;
-          uint16_t* const dst = p.out + (trow * p.n_head + head) * HD;
+          float inv[2];
+          uint16_t* dst[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            inv[x] = l[x] > 0.f ? 1.0f / l[x] : 0.f;
+            const int mr = lane0 + lane / 4 + 8 * x, tok_in = mr / p.G;
+            const long long row = (long long)(it.row0 + (pair ? wg * p.tq : 0) + tok_in) * p.n_head + it.g * p.G +
+                                  (mr - tok_in * p.G);
+            dst[x] = p.out + row * HD + quad * 8;
+            if ((valid >> x & 1) && p.lse && quad == 0)
+              p.lse[row] = l[x] > 0.f ? (m[x] + log2f(l[x])) * LN2 : -INFINITY;
+          }
 #pragma unroll 1
-          for (int x = 0; x < HD / 32; ++x) {
-            uint32_t o[32];
-            tmem_ld32(ocol + 32 * x, o);
+          for (int y = 0; y < HD / 32; ++y) {  // 32 columns: four groups of eight
+            uint32_t o[16];
+            tmem_ld_quad4(ocol + 32 * y, o);
             tmem_wait_ld();
-            if (valid) {
-              uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * x);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                uint32_t pk[4];
+            for (int x = 0; x < 2; ++x) {
+              uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  pk[i] = pack_bf16x2(__uint_as_float(o[8 * y + 2 * i]) * inv, __uint_as_float(o[8 * y + 2 * i + 1]) * inv);
-                d4[y] = l > 0.f ? make_uint4(pk[0], pk[1], pk[2], pk[3]) : make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < 4; ++i)
+                w[i] = inv[x] > 0.f ? pack_bf16x2(__uint_as_float(o[4 * i + 2 * x]) * inv[x],
+                                                  __uint_as_float(o[4 * i + 2 * x + 1]) * inv[x])
+                                    : 0u;
+              // Four lanes hold one pair each of each of four groups; lane i of the quad is to have
+              // group i whole: a 4 x 4 transposition, so that a lane stores 16 bytes and a quad 64
+              // of its row.
+              uint32_t u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int gsel = quad ^ k;
+                const uint32_t send = gsel & 2 ? (gsel & 1 ? w[3] : w[2]) : (gsel & 1 ? w[1] : w[0]);
+                u[k] = __shfl_xor_sync(FULL, send, k);  // from lane quad ^ k its pair of group `quad`
               }
+              const uint32_t a0 = quad & 1 ? u[1] : u[0], a1 = quad & 1 ? u[0] : u[1];
+              const uint32_t a2 = quad & 1 ? u[3] : u[2], a3 = quad & 1 ? u[2] : u[3];
+              const uint4 line = quad & 2 ? make_uint4(a2, a3, a0, a1) : make_uint4(a0, a1, a2, a3);
+              if (valid >> x & 1) *reinterpret_cast<uint4*>(dst[x] + y * 32) = line;
             }
           }
-          if (valid && p.lse) p.lse[trow * p.n_head + head] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
         } else {
           uint8_t* const part = p.parts + (size_t)it.part * PART_BYTES;
-          const int prow = (pair ? wg * 128 : 0) + m_row;
-          float4* const po = reinterpret_cast<float4*>(part) + prow;
+          const int prow = (pair ? wg * 128 : 0) + lane0 + lane / 4;
+          float2* const po = reinterpret_cast<float2*>(part) + prow * 4 + quad;
 #pragma unroll 1
-          for (int x = 0; x < HD / 32; ++x) {
-            uint32_t o[32];
-            tmem_ld32(ocol + 32 * x, o);
+          for (int y = 0; y < HD / 32; ++y) {
+            uint32_t o[16];
+            tmem_ld_quad4(ocol + 32 * y, o);
             tmem_wait_ld();
-            if (valid) {
 #pragma unroll
-              for (int y = 0; y < 8; ++y)
-                po[(x * 8 + y) * 256] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
-                                                    __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+            for (int i = 0; i < 8; ++i)
+              if (valid >> (i & 1) & 1)
+                po[(y * 4 + (i >> 1)) * 1024 + (i & 1) * 32] =
+                    make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          }
+          float* const ml = reinterpret_cast<float*>(part + PART_O) + prow;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if ((valid >> x & 1) && quad == 0) {
+              ml[8 * x] = m[x];
+              ml[256 + 8 * x] = l[x];
             }
-          }
-          if (valid) {
-            float* const ml = reinterpret_cast<float*>(part + PART_O);
-            ml[prow] = m;
-            ml[256 + prow] = l;
-          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[slot]));
       tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
@@ -695,75 +828,84 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 
 // Joins the partials of the work tile that begins in range blockIdx.x and ends in a later one:
 // out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over its parts in the order of the keys
-// (slot 2 c + 1 of the first CTA, slots 2 c of the others).  One block per 16 rows.
+// (slot 2 c + 1 of the first CTA, slots 2 c of the others).  A block takes groups of 16 rows;
+// with fewer rows (a decode token has G) its threads share the parts of a row instead, each
+// sums every n-th one and the sums are added in a fixed order.
 constexpr int COMBINE_ROWS = 16;
 constexpr int COMBINE_THREADS = 512;
+constexpr int COMBINE_BLOCKS = 4;  // per work tile: one wave of 512-thread blocks
 __global__ void __launch_bounds__(COMBINE_THREADS) paged_combine_kernel(const __grid_constant__ PagedParams p) {
   __shared__ float s_w[CTAS][COMBINE_ROWS];  // each part's weight per row
   __shared__ float s_inv[COMBINE_ROWS];
+  __shared__ float4 s_sum[COMBINE_THREADS];
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x;
   const Split s = p.splits[c];
   if (s.last < 0) return;
   const int nparts = s.last - c + 1;
-  // The rows of this block: row m of half h is token h tq + m / G, head m % G.
-  const int h = (int)blockIdx.y / (128 / COMBINE_ROWS), m0 = (int)blockIdx.y % (128 / COMBINE_ROWS) * COMBINE_ROWS;
-  const int used = min(max(s.ntok - h * p.tq, 0), p.tq) * p.G;  // rows in use of the half
-  const int rows = min(COMBINE_ROWS, used - m0);
-  if (rows <= 0) return;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * PART_BYTES; };
-  const int prow = h * 128 + m0;
-  auto row_of = [&](int r, long long& trow, int& head) {
-    const int m = m0 + r, tok = m / p.G;
-    trow = s.row0 + h * p.tq + tok;
-    head = s.g * p.G + (m - tok * p.G);
-  };
-  // One warp per row: the largest maximum, the weights, the sum.
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (warp < rows) {
-    float top = -INFINITY;
-    for (int i = lane; i < nparts; i += 32)
-      top = fmaxf(top, reinterpret_cast<const float*>(part(i) + PART_O)[prow + warp]);
+  for (int group = blockIdx.y; group < 256 / COMBINE_ROWS; group += COMBINE_BLOCKS) {
+    // Row m of half h is token h tq + m / G, head m % G.
+    const int h = group / (128 / COMBINE_ROWS), m0 = group % (128 / COMBINE_ROWS) * COMBINE_ROWS;
+    const int used = min(max(s.ntok - h * p.tq, 0), p.tq) * p.G;  // rows in use of the half
+    const int rows = min(COMBINE_ROWS, used - m0);
+    if (rows <= 0) continue;
+    const int prow = h * 128 + m0;
+    auto out_row = [&](int r) {
+      const int m = m0 + r, tok = m / p.G;
+      return (long long)(s.row0 + h * p.tq + tok) * p.n_head + s.g * p.G + (m - tok * p.G);
+    };
+    __syncthreads();  // the group before is done with the shared arrays
+    // One warp per row: the largest maximum, the weights, the sum.
+    if (warp < rows) {
+      float top = -INFINITY;
+      for (int i = lane; i < nparts; i += 32)
+        top = fmaxf(top, reinterpret_cast<const float*>(part(i) + PART_O)[prow + warp]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-    float sum = 0.f;
-    for (int i = lane; i < nparts; i += 32) {
-      const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
-      const float mi = ml[prow + warp];
-      const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
-      s_w[i][warp] = w;
-      sum += w * ml[256 + prow + warp];
-    }
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+      float sum = 0.f;
+      for (int i = lane; i < nparts; i += 32) {
+        const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
+        const float mi = ml[prow + warp];
+        const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
+        s_w[i][warp] = w;
+        sum += w * ml[256 + prow + warp];
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-    if (lane == 0) {
-      s_inv[warp] = sum > 0.f ? 1.0f / sum : 0.f;
-      if (p.lse) {
-        long long trow;
-        int head;
-        row_of(warp, trow, head);
-        p.lse[trow * p.n_head + head] = sum > 0.f ? (top + log2f(sum)) * LN2 : -INFINITY;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+      if (lane == 0) {
+        s_inv[warp] = sum > 0.f ? 1.0f / sum : 0.f;
+        if (p.lse) p.lse[out_row(warp)] = sum > 0.f ? (top + log2f(sum)) * LN2 : -INFINITY;
       }
     }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < rows * 32; e += COMBINE_THREADS) {
-    const int r = e % rows, c4 = e / rows;  // neighbouring threads, neighbouring rows
+    __syncthreads();
+    // float4 e of the group: two per row and group of eight columns, rows together.
+    const int elems = rows * 32, share = COMBINE_THREADS / elems;  // threads per element
+    const int e = tid % elems, first = tid / elems;
+    const int r = (e >> 1) % rows, c8 = (e >> 1) / rows;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < nparts; ++i) {
-      const float w = s_w[i][r];
-      if (w != 0.f) {
-        const float4 x = reinterpret_cast<const float4*>(part(i))[c4 * 256 + prow + r];
-        o = make_float4(o.x + w * x.x, o.y + w * x.y, o.z + w * x.z, o.w + w * x.w);
+    if (first < share) {
+      const size_t at = ((size_t)c8 * 256 + prow + r) * 2 + (e & 1);
+#pragma unroll 4
+      for (int i = first; i < nparts; i += share) {
+        const float w = s_w[i][r];
+        const float4 x = reinterpret_cast<const float4*>(part(i))[at];
+        if (w != 0.f) o = make_float4(o.x + w * x.x, o.y + w * x.y, o.z + w * x.z, o.w + w * x.w);
       }
     }
-    const float inv = s_inv[r];
-    long long trow;
-    int head;
-    row_of(r, trow, head);
-    reinterpret_cast<uint2*>(p.out + (trow * p.n_head + head) * HD)[c4] =
-        inv > 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+    s_sum[tid] = o;
+    __syncthreads();
+    if (first == 0) {
+      for (int i = 1; i < share; ++i) {
+        const float4 x = s_sum[i * elems + e];
+        o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+      }
+      const float inv = s_inv[r];
+      reinterpret_cast<uint2*>(p.out + out_row(r) * HD)[c8 * 2 + (e & 1)] =
+          inv > 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+    }
   }
 }
 
@@ -780,6 +922,7 @@ cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q
   p.G = s.n_head / s.n_kv_head;
   p.tq = 128;
   while (p.tq * p.G > 128) p.tq >>= 1;  // 128 / (G rounded up to a power of two)
+  while ((1 << p.tQ_shift) < 2 * p.tq) ++p.tQ_shift;
   while ((1 << p.page_shift) < s.page_size) ++p.page_shift;
   const uint64_t qdims[4] = {64, 2, (uint64_t)s.n_head, (uint64_t)s.tokens};
   const uint64_t qstrides[3] = {128, 256, (uint64_t)q_stride * 2};
@@ -809,7 +952,7 @@ cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q
   cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e == cudaSuccess) e = launch_pdl(paged_attention_kernel, dim3(CTAS), dim3(THREADS), SMEM_BYTES, st, p);
   if (e == cudaSuccess)
-    e = launch_pdl(paged_combine_kernel, dim3(CTAS, 2 * 128 / COMBINE_ROWS), dim3(COMBINE_THREADS), 0, st, p);
+    e = launch_pdl(paged_combine_kernel, dim3(CTAS, COMBINE_BLOCKS), dim3(COMBINE_THREADS), 0, st, p);
   return e;
 }
 
