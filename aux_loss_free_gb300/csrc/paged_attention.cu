@@ -175,6 +175,58 @@ struct SmemState {
 };
 static_assert(sizeof(SmemState) <= SMEM_BYTES - STATE_OFF, "the state fits behind the ring");
 
+// A ring stage and the parity of its use; the next one.
+struct Ring {
+  uint32_t stage, phase;
+  __device__ __forceinline__ Ring next() const {
+    return stage + 1 == STAGES ? Ring{0, phase ^ 1u} : Ring{stage + 1, phase};
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// Whether three phases are done (give one twice for two); the tests are on their way together.
+__device__ __forceinline__ bool mbar_test_all(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2,
+                                              uint32_t p2) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\t"
+      "and.pred p, p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(b2), "r"(p2)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait for three phases.
+__device__ __forceinline__ bool mbar_wait_all(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2,
+                                              uint32_t p2, int* status) {
+  unsigned long long t0 = 0;
+  while (true) {
+    for (int i = 0; i < 256; ++i)
+      if (mbar_test_all(b0, p0, b1, p1, b2, p2)) return true;
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitLimitNs) {
+      atomicOr(status, kDevTimeout);
+      return false;
+    }
+  }
+}
+
 // Warp-wide wait by lane 0.
 __device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, int* status) {
   int w = 1;
@@ -192,18 +244,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // TMEM in the 16 x 256-bit shape: sixteen rows, `n` groups of eight fp32 columns; a lane holds
 // columns 2 (lane % 4) + {0, 1} of every group of rows lane / 4 (registers 4 g, 4 g + 1) and
 // lane / 4 + 8 (4 g + 2, 4 g + 3).
-__device__ __forceinline__ void tmem_ld_quad8(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld_quad4(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
@@ -213,6 +253,23 @@ __device__ __forceinline__ void tmem_ld_quad4(uint32_t taddr, uint32_t (&r)[16])
       : "r"(taddr)
       : "memory");
 }
+// Wait for this warp's TMEM loads; the registers they fill are operands, so that nothing that
+// uses them moves before it.
+__device__ __forceinline__ void tmem_wait_quad4(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_quad4(uint32_t (&r)[16], uint32_t (&q)[16]) {
+  tmem_wait_quad4(r);
+  asm volatile(""
+               : "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]), "+r"(q[4]), "+r"(q[5]), "+r"(q[6]), "+r"(q[7]),
+                 "+r"(q[8]), "+r"(q[9]), "+r"(q[10]), "+r"(q[11]), "+r"(q[12]), "+r"(q[13]), "+r"(q[14]), "+r"(q[15])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_quad4(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
@@ -221,14 +278,12 @@ __device__ __forceinline__ void tmem_st_quad4(uint32_t taddr, const uint32_t (&r
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// The 16 x 128-bit shape, eight groups of four 32-bit columns: column lane % 4 of every group of
+// The 16 x 128-bit shape, four groups of four 32-bit columns: column lane % 4 of every group of
 // rows lane / 4 (register 2 g) and lane / 4 + 8 (2 g + 1): the bf16 pairs of the shape above.
-__device__ __forceinline__ void tmem_st_pairs8(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st_pairs4(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 
@@ -463,114 +518,116 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     for (uint32_t l = loads > STAGES ? loads - STAGES : 0; l < loads; ++l)
       warp_wait(&sm.ring_full[l % STAGES], l / STAGES, p.status);
   } else if (warp == MMA_WARP) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      constexpr uint32_t id_s = idesc_bf16_f32(128, BK, 0, 0);
-      constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, 0, 1);
-      uint32_t q_uses[2] = {0, 0}, tiles = 0, pairs = 0, even = 0, odd = 0;
-      auto wait = [&](const uint64_t* bar, uint32_t parity) {
-        return mbar_wait_spin(smem_u32(bar), parity & 1u, p.status);
-      };
-      auto score = [&](int half, int buf, int st) {  // S[buf] = Q[half] K^T
-        const uint64_t qd = sw128_kmajor_desc(base + half * TILE_BYTES);
-        const uint64_t kd = sw128_kmajor_desc(base + RING_OFF + st * TILE_BYTES);
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the items, so that descriptors are built in uniform registers; one
+    // elected lane issues.  A barrier test costs some 250 cycles while the tensor pipe reads
+    // shared memory, and the pipe holds about four products (both measured): one test for all
+    // that a step needs.
+    constexpr uint32_t id_s = idesc_bf16_f32(128, BK, 0, 0);
+    constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, 0, 1);
+    const bool issues = elect_one();
+    uint32_t q_uses[2] = {0, 0}, pairs = 0, even = 0, odd = 0;
+    Ring key{0, 0};  // of the next key tile; its value tile is the stage behind
+    auto score = [&](int half, int buf, uint32_t st) {  // S[buf] = Q[half] K^T
+      const uint64_t qd = sw128_kmajor_desc(base + half * TILE_BYTES);
+      const uint64_t kd = sw128_kmajor_desc(base + RING_OFF + st * TILE_BYTES);
+      if (issues) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           tc_mma_bf16(tmem + buf * BK, qd + (kk >> 2) * (ATOM_BYTES >> 4) + 2 * (kk & 3),
                       kd + (kk >> 2) * (ATOM_BYTES >> 4) + 2 * (kk & 3), id_s, kk != 0);
-      };
-      auto value = [&](int out, int buf, int st, bool first) {  // O[out] (+)= P[buf] V
-        const uint64_t vd = sw128_mnmajor_desc(base + RING_OFF + st * TILE_BYTES, ATOM_BYTES);
+      }
+    };
+    auto value = [&](int out, int buf, uint32_t st, bool first) {  // O[out] (+)= P[buf] V
+      const uint64_t vd = sw128_mnmajor_desc(base + RING_OFF + st * TILE_BYTES, ATOM_BYTES);
+      if (issues) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
           tc_mma_bf16_a_tmem(tmem + O_COL + out * HD, tmem + buf * BK + (kk >> 2) * 64 + (kk & 3) * 8,
                              vd + kk * 128u, id_pv, !first || kk != 0);
-      };
-      for (uint32_t items = 0;; ++items) {
-        const int slot = items % ITEMS;
-        if (!wait(&sm.item_full[slot], items / ITEMS)) break;
-        const int nt = sm.items[slot].nt, half = sm.items[slot].half;
-        mbar_arrive(smem_u32(&sm.item_empty[slot]));
-        if (nt == 0) break;
-        const bool pair = half == 2;
-        bool ok = true;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (ok && (pair || half == h)) ok = wait(&sm.q_full[h], q_uses[h]++);
-        // Key tile t of the item is load 2 (tiles + t), its value tile the next one.
-        auto ready = [&](int t, int kv) {
-          const uint32_t l = 2 * (tiles + t) + kv;
-          return wait(&sm.ring_full[l % STAGES], l / STAGES);
-        };
-        auto stage = [&](int t, int kv) { return (int)((2 * (tiles + t) + kv) % STAGES); };
-        if (!ok || !ready(0, 0)) break;
-        tc_fence_after();
-        if (pair) {
-          for (int h = 0; h < 2; ++h) {
-            score(h, h, stage(0, 0));
-            tc_commit(smem_u32(&sm.s_full[h]));
-          }
-          tc_commit(smem_u32(&sm.ring_empty[stage(0, 0)]));
-          for (int t = 0; t < nt && ok; ++t) {
-            const bool more = t + 1 < nt;
-            for (int h = 0; h < 2; ++h) {
-              if (!wait(&sm.p_full[h], pairs + t) || (h == 0 && !ready(t, 1))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              value(h, h, stage(t, 1), t == 0);
-              if (h == 1) tc_commit(smem_u32(&sm.ring_empty[stage(t, 1)]));
-              if (more) {
-                if (h == 0 && !ready(t + 1, 0)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                score(h, h, stage(t + 1, 0));
-                tc_commit(smem_u32(&sm.s_full[h]));  // covers the value product before it
-                if (h == 1) tc_commit(smem_u32(&sm.ring_empty[stage(t + 1, 0)]));
-              } else {
-                tc_commit(smem_u32(&sm.o_full[h]));
-                if (h == 1)
-                  for (int x = 0; x < 2; ++x) tc_commit(smem_u32(&sm.q_empty[x]));
-              }
-            }
-          }
-          pairs += nt;
-        } else {
-          score(half, 0, stage(0, 0));
-          tc_commit(smem_u32(&sm.s_full[2]));
-          tc_commit(smem_u32(&sm.ring_empty[stage(0, 0)]));
-          for (int t = 0; t < nt; ++t) {
-            const int b = t & 1;
-            if (t + 1 < nt) {
-              if (!ready(t + 1, 0)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              score(half, b ^ 1, stage(t + 1, 0));
-              tc_commit(smem_u32(&sm.s_full[2 + (b ^ 1)]));
-              tc_commit(smem_u32(&sm.ring_empty[stage(t + 1, 0)]));
-            }
-            if (t + 1 == nt) tc_commit(smem_u32(&sm.q_empty[half]));  // every score product is issued
-            if (!wait(&sm.p_full[2 + b], (b ? odd : even) + (t >> 1)) || !ready(t, 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            value(0, b, stage(t, 1), t == 0);
-            tc_commit(smem_u32(&sm.ring_empty[stage(t, 1)]));
-            tc_commit(smem_u32(&sm.pv_done[b]));
-            if (t + 1 == nt) tc_commit(smem_u32(&sm.o_full[0]));
-          }
-          even += (nt + 1) >> 1;
-          odd += nt >> 1;
-        }
-        if (!ok) break;
-        tiles += nt;
       }
+    };
+    auto commit = [&](const uint64_t* bar) {
+      if (issues) tc_commit(smem_u32(bar));
+    };
+    for (uint32_t items = 0;; ++items) {
+      const int slot = items % ITEMS;
+      if (!warp_wait(&sm.item_full[slot], items / ITEMS, p.status)) break;
+      const int nt = __shfl_sync(FULL, sm.items[slot].nt, 0), half = __shfl_sync(FULL, sm.items[slot].half, 0);
+      if (issues) mbar_arrive(smem_u32(&sm.item_empty[slot]));
+      if (nt == 0) break;
+      const bool pair = half == 2;
+      const uint32_t q0 = smem_u32(&sm.q_full[half == 1]), q0_phase = (half == 1 ? q_uses[1] : q_uses[0]) & 1u;
+      const uint32_t q1 = pair ? smem_u32(&sm.q_full[1]) : q0, q1_phase = pair ? q_uses[1] & 1u : q0_phase;
+      q_uses[0] += pair || half == 0;
+      q_uses[1] += pair || half == 1;
+      auto full = [&](const Ring& r) { return smem_u32(&sm.ring_full[r.stage]); };
+      if (!mbar_wait_all(full(key), key.phase, q0, q0_phase, q1, q1_phase, p.status)) break;
+      tc_fence_after();
+      bool ok = true;
+      if (pair) {
+        for (int h = 0; h < 2; ++h) {
+          score(h, h, key.stage);
+          commit(&sm.s_full[h]);
+        }
+        commit(&sm.ring_empty[key.stage]);
+        for (int t = 0; t < nt; ++t) {
+          const bool more = t + 1 < nt;
+          const Ring val = key.next(), next = val.next(), last = more ? next : val;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // P, and in front of the first half the value tile and the next key tile.
+            const uint32_t pf = smem_u32(&sm.p_full[h]), pp = (pairs + t) & 1u;
+            ok = ok && (h == 0 ? mbar_wait_all(pf, pp, full(val), val.phase, full(last), last.phase, p.status)
+                               : mbar_wait_all(pf, pp, pf, pp, pf, pp, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            value(h, h, val.stage, t == 0);
+            if (more) {
+              score(h, h, next.stage);
+              commit(&sm.s_full[h]);  // covers the value product before it
+            } else {
+              commit(&sm.o_full[h]);
+              commit(&sm.q_empty[h]);
+            }
+          }
+          if (!ok) break;
+          commit(&sm.ring_empty[val.stage]);
+          if (more) commit(&sm.ring_empty[next.stage]);
+          key = next;
+        }
+        pairs += nt;
+      } else {
+        score(half, 0, key.stage);
+        commit(&sm.s_full[2]);
+        commit(&sm.ring_empty[key.stage]);
+        for (int t = 0; t < nt; ++t) {
+          const int b = t & 1;
+          const Ring val = key.next(), next = val.next();
+          if (t + 1 < nt) {
+            ok = mbar_wait_all(full(next), next.phase, full(next), next.phase, full(next), next.phase, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            score(half, b ^ 1, next.stage);
+            commit(&sm.s_full[2 + (b ^ 1)]);
+            commit(&sm.ring_empty[next.stage]);
+          } else {
+            commit(&sm.q_empty[half]);  // every score product is issued
+          }
+          const uint32_t pf = smem_u32(&sm.p_full[2 + b]), pp = ((b ? odd : even) + (t >> 1)) & 1u;
+          ok = mbar_wait_all(pf, pp, full(val), val.phase, pf, pp, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          value(0, b, val.stage, t == 0);
+          if (t + 1 == nt) commit(&sm.o_full[0]);
+          commit(&sm.pv_done[b]);
+          commit(&sm.ring_empty[val.stage]);
+          key = next;
+        }
+        even += (nt + 1) >> 1;
+        odd += nt >> 1;
+      }
+      if (!ok) break;
     }
   } else {
     // ------------------------------------------------------------ softmax warps
@@ -620,34 +677,56 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         }
         tc_fence_after();
         const int k0 = first_key + t * BK;
+        if (k0 + BK > kvlim) {
+          // Values that no row of the tile may see: rows kvlim - k0 .. 127 of the stage.
+          const uint32_t vl = 2 * (tiles + t) + 1;
+          if (!warp_wait(&sm.ring_full[vl % STAGES], vl / STAGES, p.status)) {
+            ok = false;
+            break;
+          }
+          const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
+          if (zrow >= kvlim - k0) {
+            uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + zcol * ATOM_BYTES +
+                                                      zrow * 128);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) z[x] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+        }
         if (active) {
-          // Two halves of 64 keys.  The maximum needs both; the first is read again for its
-          // exponentials, so that one half is in registers at a time (96 a thread: 16 warps).
+          // The maximum needs all 128 keys, in two loads of 64; the second one's stay in
+          // registers, the first one's are read again for their exponentials, 32 keys at a time
+          // behind the arithmetic (96 registers a thread, for 16 warps).
           const bool edge = __any_sync(FULL, min(limit[0], limit[1]) < k0 + BK);
-          uint32_t v[32];
-          auto mask = [&](int y) {
+          uint32_t va[16], vb[16];  // 32 keys each
+          auto mask = [&](uint32_t(&v)[16], int y) {
             if (edge) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (k0 + 64 * y + (i >> 2) * 8 + quad * 2 + (i & 1) >= limit[(i >> 1) & 1])
+              for (int i = 0; i < 16; ++i)
+                if (k0 + 32 * y + (i >> 2) * 8 + quad * 2 + (i & 1) >= limit[(i >> 1) & 1])
                   v[i] = __float_as_uint(-INFINITY);
             }
+          };
+          auto row_max = [&](const uint32_t(&v)[16], int x) {
+            float mx[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = fmaxf(__uint_as_float(v[4 * i + 2 * x]), __uint_as_float(v[4 * i + 2 * x + 1]));
+              mx[i & 1] = i < 2 ? a : fmaxf(mx[i & 1], a);
+            }
+            return fmaxf(mx[0], mx[1]);
           };
           float tmax[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            tmem_ld_quad8(scol + 64 * y, v);
-            tmem_wait_ld();
-            mask(y);
+            tmem_ld_quad4(scol + 64 * y, va);
+            tmem_ld_quad4(scol + 64 * y + 32, vb);
+            tmem_wait_quad4(va, vb);
+            mask(va, 2 * y);
+            mask(vb, 2 * y + 1);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float mx[2];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float a = fmaxf(__uint_as_float(v[4 * i + 2 * x]), __uint_as_float(v[4 * i + 2 * x + 1]));
-                mx[i & 1] = i < 2 ? a : fmaxf(mx[i & 1], a);
-              }
-              const float a = fmaxf(mx[0], mx[1]);
+              const float a = fmaxf(row_max(va, x), row_max(vb, x));
               tmax[x] = y ? fmaxf(tmax[x], a) : a;
             }
           }
@@ -679,7 +758,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             for (int x = 0; x < HD / 32; ++x) {
               uint32_t o[16];
               tmem_ld_quad4(ocol + 32 * x, o);
-              tmem_wait_ld();
+              tmem_wait_quad4(o);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor[(i >> 1) & 1]);
               tmem_st_quad4(ocol + 32 * x, o);
@@ -689,16 +768,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           // 2^(s scale - m); a row without keys so far has m = -inf and only masked scores.
           const float mu0 = m[0] == -INFINITY ? 0.f : -m[0], mu1 = m[1] == -INFINITY ? 0.f : -m[1];
           float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto weights = [&](const uint32_t(&v)[16], int y) {  // P of 32 keys, over the scores of half y / 2
+            uint32_t pk[8];
 #pragma unroll
-          for (int y = 1; y >= 0; --y) {
-            if (y == 0) {
-              tmem_ld_quad8(scol, v);
-              tmem_wait_ld();
-              mask(0);
-            }
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const int x = i & 1;
               const float mu = x ? mu1 : mu0;
               const float2 a = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2,
@@ -707,27 +780,22 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               ls[x] = __fadd2_rn(ls[x], e);
               pk[i] = pack_bf16x2(e.x, e.y);
             }
-            tmem_st_pairs8(scol + 64 * y, pk);  // over the half's own scores
-          }
+            tmem_st_pairs4(scol + (y >> 1) * 64 + (y & 1) * 16, pk);
+          };
+          // P of keys 64 .. 127 lies over their own scores (columns 64 .. 95); P of keys 0 .. 63
+          // over columns 0 .. 31, whose scores are in registers by then.
+          weights(va, 2);
+          tmem_ld_quad4(scol, va);
+          weights(vb, 3);
+          tmem_ld_quad4(scol + 32, vb);
+          tmem_wait_quad4(va, vb);
+          mask(va, 0);
+          mask(vb, 1);
+          weights(va, 0);
+          weights(vb, 1);
           l[0] += ls[0].x + ls[0].y;
           l[1] += ls[1].x + ls[1].y;
           tmem_wait_st();  // P is in TMEM before the MMA may read it
-        }
-        if (k0 + BK > kvlim) {
-          // Values that no row of the tile may see: rows kvlim - k0 .. 127 of the stage.
-          const uint32_t vl = 2 * (tiles + t) + 1;
-          if (!warp_wait(&sm.ring_full[vl % STAGES], vl / STAGES, p.status)) {
-            ok = false;
-            break;
-          }
-          const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
-          if (zrow >= kvlim - k0) {
-            uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + zcol * ATOM_BYTES +
-                                                      zrow * 128);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) z[x] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-          }
         }
         tc_fence_before();
         __syncwarp();
@@ -764,7 +832,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           for (int y = 0; y < HD / 32; ++y) {  // 32 columns: four groups of eight
             uint32_t o[16];
             tmem_ld_quad4(ocol + 32 * y, o);
-            tmem_wait_ld();
+            tmem_wait_quad4(o);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               uint32_t w[4];
@@ -797,7 +865,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           for (int y = 0; y < HD / 32; ++y) {
             uint32_t o[16];
             tmem_ld_quad4(ocol + 32 * y, o);
-            tmem_wait_ld();
+            tmem_wait_quad4(o);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (valid >> (i & 1) & 1)
