@@ -148,13 +148,17 @@ def load_library(path: str = LIB_PATH):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The stream's handle; by default PyTorch's current stream of the current device.  Read
+    from PyTorch's own per-device word (0.3 us): building a Stream object for it takes 3 us, as
+    long as a launch."""
+    if stream is not None:
+        return stream.cuda_stream
+    from torch import _C
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
 
 
 def _check(name: str, code: int):

@@ -119,7 +119,7 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 
 // Request r; r == R is the padding rows.  Lengths out of range are reported once per call
 // (`report`) and leave a request without keys or without rows.
-__device__ Request load_request(const PagedParams& p, int r, bool report) {
+__device__ __forceinline__ Request load_request(const PagedParams& p, int r, bool report) {
   Request q;
   const int a = p.row_start[r], b = r < p.R ? p.row_start[r + 1] : p.T;
   const bool rows_ok = a >= 0 && a <= b && b <= p.T;
@@ -156,6 +156,7 @@ __device__ __forceinline__ int key_tiles(const Request& q, int i, int tQ_shift) 
 // Units of one key/value head of the request.
 __device__ __forceinline__ long long head_units(const Request& q, int tQ_shift) {
   if (q.qn == 0) return 0;
+  if (q.qn == 1) return key_tiles(q, 0, tQ_shift) + 1;
   return units_of_full(q, q.qn - 1, tQ_shift) + key_tiles(q, q.qn - 1, tQ_shift) + 1;
 }
 
@@ -239,6 +240,25 @@ __device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The same for the eight warps of a query half (hardware barrier 1 + wg): one lane of the first
+// warp polls, the others sleep at the barrier, which hands them the outcome.  Sixteen polling
+// warps slow the loading and the issuing warp down several times (measured: 2.4 us instead of
+// 0.4 us for the walk's start).
+__device__ __forceinline__ bool half_wait(const uint64_t* bar, uint32_t parity, int wg, int* status) {
+  uint32_t ok = 1;
+  if (threadIdx.x % 256 == 0) ok = mbar_wait(smem_u32(bar), parity & 1u, status) ? 1 : 0;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok)
+      : "r"(ok), "r"(1 + wg)
+      : "memory");
+  return ok != 0;
 }
 
 // TMEM in the 16 x 256-bit shape: sixteen rows, `n` groups of eight fp32 columns; a lane holds
@@ -362,7 +382,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   const int ctas = (int)min((long long)gridDim.x, total);  // every range holds a unit
   const int c = blockIdx.x;
   const bool working = c < ctas;
-  const long long u0 = working ? div_ll(total * c, ctas) : 0, u1 = working ? div_ll(total * (c + 1), ctas) : 0;
+  const bool one = total == ctas;  // a unit each: no division
+  const long long u0 = !working ? 0 : one ? c : div_ll(total * c, ctas);
+  const long long u1 = !working ? 0 : one ? c + 1 : div_ll(total * (c + 1), ctas);
   if (working && mine > 0 && u0 >= upto - mine && u0 < upto) {
     long long at = upto - mine;
     for (int r = r0; r < r1; ++r) {
@@ -375,12 +397,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       at += w;
     }
   }
-  if (tid == 0) p.splits[c].last = -1;
   __syncthreads();
   const uint32_t tmem = sm.tmem;
 
-  if (!working) {
-  } else if (warp == LOAD_WARP) {
+  if (warp == LOAD_WARP) {
     // ------------------------------------------------------------ walk and TMA copies
     const int nb = BK >> p.page_shift;         // pages per key tile
     const int box = lane & (nb - 1), col = lane >= nb ? 1 : 0;
@@ -388,13 +408,18 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     const uint32_t box_dst = col * ATOM_BYTES + (box << p.page_shift) * 128;
     const uint32_t q_bytes = (uint32_t)(2 * p.tq * p.G * 128);
     const int rows_end = (int)((long long)p.pages * p.n_kv_head << p.page_shift);  // out of range: zeros
-    int r = sm.start_req;
-    Request q = load_request(p, r, false);
-    const long long w = head_units(q, p.tQ_shift);
-    int g = (int)div_ll(sm.start_off, w);
-    const long long off = sm.start_off - g * w;
+    int r = working ? sm.start_req : 0;
+    long long off = working ? sm.start_off : 0;
+    Request q{};
+    int g = 0;
     int i = 0;  // the work tile that holds unit `off` of the head: units_of_full(i) <= off
-    {
+    if (working) {
+      q = load_request(p, r, false);
+      const long long units = head_units(q, p.tQ_shift);
+      while (off >= units) {
+        off -= units;
+        ++g;
+      }
       int hi = q.qn;
       while (hi - i > 1) {
         const int mid = (i + hi) >> 1;
@@ -406,6 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     long long unit = u0;
     uint32_t items = 0, loads = 0, q_uses[2] = {0, 0};
     int next_half = 0;
+    Split split{0, 0, 0, -1};
     bool ok = true;
     while (ok && unit < u1) {
       const int tile_n = key_tiles(q, i, p.tQ_shift);
@@ -437,8 +463,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         }
         __syncwarp();
         ++items;
-        // The key and value tiles, one box per page and column half and lane; the query
-        // halves behind the first key tile.
+        // The key and value tiles, one box per page and column half and lane; the query halves
+        // behind the first key tile.
         for (int t = 0; t < it.nt && ok; ++t) {
           const bool there = ((long long)((it.j0 + t) * nb + box) << p.page_shift) < it.kvlim;
           int coord = rows_end;
@@ -480,15 +506,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           }
         }
         if (it.half != 2) next_half = it.half ^ 1;
-        if (j == 0 && !ends && lane == 0) {
-          // The unit after the tile's last key tile belongs to CTA ((u + 1) ctas - 1) / total.
-          Split s;
-          s.row0 = it.row0;
-          s.ntok = it.ntok;
-          s.g = g;
-          s.last = (int)div_ll((unit + tile_n) * ctas - 1, total);
-          p.splits[c] = s;
-        }
+        // Unit u belongs to CTA ((u + 1) ctas - 1) / total: the tile's last key tile.
+        if (j == 0 && !ends) split = Split{it.row0, it.ntok, g, (int)div_ll((unit + tile_n) * ctas - 1, total)};
       }
       unit += units;
       // The next work tile: query tile, then head, then request.
@@ -504,6 +523,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         }
       }
     }
+    if (lane == 0) p.splits[c] = split;
     if (ok) {  // nt == 0 ends the walk
       const int slot = items % ITEMS;
       if (warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status) && lane == 0) {
@@ -640,7 +660,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     bool ok = true;
     for (uint32_t items = 0; ok; ++items) {
       const int slot = items % ITEMS;
-      if (!warp_wait(&sm.item_full[slot], items / ITEMS, p.status)) break;
+      if (!half_wait(&sm.item_full[slot], items / ITEMS, wg, p.status)) break;
       const Item& it = sm.items[slot];  // this warp's until it arrives at item_empty
       const int nt = it.nt;
       const bool pair = it.half == 2;
@@ -671,7 +691,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         const int sb = pair ? wg : 2 + b;            // barrier set
         const uint32_t scol = tl + (pair ? wg : b) * BK;
         const uint32_t ph = pair ? pairs + t : (b ? odd : even) + (t >> 1);
-        if (!warp_wait(&sm.s_full[sb], ph, p.status)) {
+        if (!half_wait(&sm.s_full[sb], ph, wg, p.status)) {
           ok = false;
           break;
         }
@@ -680,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (k0 + BK > kvlim) {
           // Values that no row of the tile may see: rows kvlim - k0 .. 127 of the stage.
           const uint32_t vl = 2 * (tiles + t) + 1;
-          if (!warp_wait(&sm.ring_full[vl % STAGES], vl / STAGES, p.status)) {
+          if (!half_wait(&sm.ring_full[vl % STAGES], vl / STAGES, wg, p.status)) {
             ok = false;
             break;
           }
@@ -746,11 +766,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             }
           }
           if (__any_sync(FULL, grow)) {
-            // Every earlier value product has to be done: a pair's score commit covers it.
-            if (!pair && !warp_wait(&sm.pv_done[b ^ 1], (b ? even : odd) + ((t - 1) >> 1), p.status)) {
-              ok = false;
-              break;
-            }
+            // Every earlier value product has to be done: a pair's score commit covers it.  A wait
+            // that gives up has set the status; the warp goes on, since its half waits together.
+            if (!pair) warp_wait(&sm.pv_done[b ^ 1], (b ? even : odd) + ((t - 1) >> 1), p.status);
             tc_fence_after();
             l[0] *= factor[0];
             l[1] *= factor[1];
@@ -812,7 +830,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       // ---- the item's output: O / l, or the partial
       l[0] = quad_sum(l[0]);
       l[1] = quad_sum(l[1]);
-      if (!warp_wait(&sm.o_full[wg], outs++, p.status)) break;
+      if (!half_wait(&sm.o_full[wg], outs++, wg, p.status)) break;
       tc_fence_after();
       if (active) {
         if (it.part < 0) {
@@ -894,85 +912,128 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   }
 }
 
-// Joins the partials of the work tile that begins in range blockIdx.x and ends in a later one:
+// Joins the partials of the work tile that begins in range blockIdx.y and ends in a later one:
 // out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over its parts in the order of the keys
-// (slot 2 c + 1 of the first CTA, slots 2 c of the others).  A block takes groups of 16 rows;
-// with fewer rows (a decode token has G) its threads share the parts of a row instead, each
-// sums every n-th one and the sums are added in a fixed order.
-constexpr int COMBINE_ROWS = 16;
-constexpr int COMBINE_THREADS = 512;
-constexpr int COMBINE_BLOCKS = 4;  // per work tile: one wave of 512-thread blocks
-__global__ void __launch_bounds__(COMBINE_THREADS) paged_combine_kernel(const __grid_constant__ PagedParams p) {
-  __shared__ float s_w[CTAS][COMBINE_ROWS];  // each part's weight per row
-  __shared__ float s_inv[COMBINE_ROWS];
+// (slot 2 c + 1 of the first CTA, slots 2 c of the others).  Eight blocks per work tile: of 32
+// rows each, or, where it has no more rows than that (a decode token has G, and up to 152
+// parts), of two column groups each; there the threads share the parts of an element, every
+// n-th one each, and their sums are added in a fixed order.  The first loads of O are on their
+// way before the weights are known.  Bound by latency: two dependent loads behind the launch.
+constexpr int COMBINE_THREADS = 256;
+constexpr int COMBINE_BLOCKS = 8;
+__global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ float s_w[CTAS][32];  // each part's weight per row
+  __shared__ float s_inv[32];
   __shared__ float4 s_sum[COMBINE_THREADS];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x;
+  const int c = blockIdx.y, bx = blockIdx.x;
   const Split s = p.splits[c];
   if (s.last < 0) return;
+  const int all = s.ntok * p.G, half0 = min(s.ntok, p.tq) * p.G;  // rows of the work tile, of its first half
+  const bool wide = all > 32;
+  const int row0 = wide ? bx * 32 : 0, rows = min(32, all - row0);
+  if (rows <= 0) return;
   const int nparts = s.last - c + 1;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * PART_BYTES; };
-  for (int group = blockIdx.y; group < 256 / COMBINE_ROWS; group += COMBINE_BLOCKS) {
-    // Row m of half h is token h tq + m / G, head m % G.
-    const int h = group / (128 / COMBINE_ROWS), m0 = group % (128 / COMBINE_ROWS) * COMBINE_ROWS;
-    const int used = min(max(s.ntok - h * p.tq, 0), p.tq) * p.G;  // rows in use of the half
-    const int rows = min(COMBINE_ROWS, used - m0);
-    if (rows <= 0) continue;
-    const int prow = h * 128 + m0;
-    auto out_row = [&](int r) {
-      const int m = m0 + r, tok = m / p.G;
-      return (long long)(s.row0 + h * p.tq + tok) * p.n_head + s.g * p.G + (m - tok * p.G);
-    };
-    __syncthreads();  // the group before is done with the shared arrays
-    // One warp per row: the largest maximum, the weights, the sum.
-    if (warp < rows) {
-      float top = -INFINITY;
-      for (int i = lane; i < nparts; i += 32)
-        top = fmaxf(top, reinterpret_cast<const float*>(part(i) + PART_O)[prow + warp]);
+  auto place = [&](int r) {  // row of the partial
+    const int m = row0 + r;
+    return m < half0 ? m : 128 + m - half0;
+  };
+  auto out_row = [&](int r) {  // row m is token m / G, head m % G
+    const int tok = (row0 + r) / p.G;
+    return (long long)(s.row0 + tok) * p.n_head + s.g * p.G + (row0 + r - tok * p.G);
+  };
+  // float4 x of row r, column group c8: two per group, 2^shift rows together.
+  int shift = 5;
+  if (!wide)
+    while (shift > 0 && 1 << (shift - 1) >= rows) --shift;
+  const int elems = wide ? 1024 : 4 << shift;  // of the block
+  const int share = wide ? 1 : COMBINE_THREADS / elems, first = wide ? 0 : tid / elems;
+  auto locate = [&](int e, int& r, int& c4) {
+    r = (e >> 1) & ((1 << shift) - 1);
+    c4 = 2 * ((e >> (shift + 1)) + (wide ? 0 : 2 * bx)) + (e & 1);
+  };
+  auto load = [&](int i, int r, int c4) {
+    return reinterpret_cast<const float4*>(part(i))[((c4 >> 1) * 256 + place(r)) * 2 + (c4 & 1)];
+  };
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 x[8];  // wide: parts 0 and 1 of four elements; else eight parts of one
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-      float sum = 0.f;
-      for (int i = lane; i < nparts; i += 32) {
-        const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
-        const float mi = ml[prow + warp];
-        const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
-        s_w[i][warp] = w;
-        sum += w * ml[256 + prow + warp];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-      if (lane == 0) {
-        s_inv[warp] = sum > 0.f ? 1.0f / sum : 0.f;
-        if (p.lse) p.lse[out_row(warp)] = sum > 0.f ? (top + log2f(sum)) * LN2 : -INFINITY;
-      }
+  for (int k = 0; k < 8; ++k) {
+    int r, c4;
+    locate(wide ? tid + (k >> 1) * COMBINE_THREADS : tid & (elems - 1), r, c4);
+    const int i = wide ? k & 1 : first + k * share;
+    x[k] = r < rows && i < nparts ? load(i, r, c4) : zero;
+  }
+  // One warp per row: the largest maximum, the weights, the sum.
+  for (int r = warp; r < rows; r += COMBINE_THREADS / 32) {
+    const int at = place(r);
+    float top = -INFINITY, mi = -INFINITY, li = 0.f;
+    for (int i = lane; i < nparts; i += 32) {
+      const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
+      mi = ml[at];
+      li = ml[256 + at];
+      top = fmaxf(top, mi);
     }
-    __syncthreads();
-    // float4 e of the group: two per row and group of eight columns, rows together.
-    const int elems = rows * 32, share = COMBINE_THREADS / elems;  // threads per element
-    const int e = tid % elems, first = tid / elems;
-    const int r = (e >> 1) % rows, c8 = (e >> 1) / rows;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (first < share) {
-      const size_t at = ((size_t)c8 * 256 + prow + r) * 2 + (e & 1);
-#pragma unroll 4
-      for (int i = first; i < nparts; i += share) {
-        const float w = s_w[i][r];
-        const float4 x = reinterpret_cast<const float4*>(part(i))[at];
-        if (w != 0.f) o = make_float4(o.x + w * x.x, o.y + w * x.y, o.z + w * x.z, o.w + w * x.w);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+    float sum = 0.f;
+    for (int i = lane; i < nparts; i += 32) {
+      if (nparts > 32) {
+        const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
+        mi = ml[at];
+        li = ml[256 + at];
       }
+      const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
+      s_w[i][r] = w;
+      sum += w * li;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    if (lane == 0) {
+      s_inv[r] = sum > 0.f ? 1.0f / sum : 0.f;
+      if (p.lse && (wide || bx == 0)) p.lse[out_row(r)] = sum > 0.f ? (top + log2f(sum)) * LN2 : -INFINITY;
+    }
+  }
+  __syncthreads();
+  auto add = [](float4& o, float w, const float4& v) {  // a weight of 0 hides what the part holds
+    if (w != 0.f) o = make_float4(o.x + w * v.x, o.y + w * v.y, o.z + w * v.z, o.w + w * v.w);
+  };
+  auto store = [&](int r, int c4, const float4& o) {
+    const float inv = s_inv[r];
+    reinterpret_cast<uint2*>(p.out + out_row(r) * HD)[c4] =
+        inv > 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+  };
+  if (wide) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      int r, c4;
+      locate(tid + k * COMBINE_THREADS, r, c4);
+      if (r >= rows) continue;
+      float4 o = zero;
+      add(o, s_w[0][r], x[2 * k]);
+      add(o, s_w[1][r], x[2 * k + 1]);
+      for (int i = 2; i < nparts; ++i) add(o, s_w[i][r], load(i, r, c4));
+      store(r, c4, o);
+    }
+  } else {
+    int r, c4;
+    locate(tid & (elems - 1), r, c4);
+    float4 o = zero;
+    if (r < rows) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (first + k * share < nparts) add(o, s_w[first + k * share][r], x[k]);
+#pragma unroll 4
+      for (int i = first + 8 * share; i < nparts; i += share) add(o, s_w[i][r], load(i, r, c4));
     }
     s_sum[tid] = o;
     __syncthreads();
-    if (first == 0) {
-      for (int i = 1; i < share; ++i) {
-        const float4 x = s_sum[i * elems + e];
-        o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-      }
-      const float inv = s_inv[r];
-      reinterpret_cast<uint2*>(p.out + out_row(r) * HD)[c8 * 2 + (e & 1)] =
-          inv > 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+    if (first == 0 && r < rows) {
+      for (int i = 1; i < share; ++i) add(o, 1.0f, s_sum[i * elems + tid]);
+      store(r, c4, o);
     }
   }
 }
@@ -1020,7 +1081,7 @@ cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q
   cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e == cudaSuccess) e = launch_pdl(paged_attention_kernel, dim3(CTAS), dim3(THREADS), SMEM_BYTES, st, p);
   if (e == cudaSuccess)
-    e = launch_pdl(paged_combine_kernel, dim3(CTAS, COMBINE_BLOCKS), dim3(COMBINE_THREADS), 0, st, p);
+    e = launch_pdl(paged_combine_kernel, dim3(COMBINE_BLOCKS, CTAS), dim3(COMBINE_THREADS), 0, st, p);
   return e;
 }
 

@@ -19,6 +19,8 @@
 // row, k and v to their page.  A copy with a reduction, bound by memory traffic.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -68,12 +70,24 @@ __device__ long long block_exclusive_sum(long long v, long long* warp_sums, long
   return before + inc - v;
 }
 
+// The last index r of the non-decreasing v[0 .. n] with v[r] <= x, where v[0] <= x < v[n].
+__device__ __forceinline__ int find_range(const int32_t* v, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanParams p) {
   extern __shared__ int32_t plan_smem[];
-  int32_t* const s_row = plan_smem;             // [R + 1] row starts, at most T
-  int32_t* const s_ctx = s_row + p.R + 1;       // [R]
-  int32_t* const s_first = s_ctx + p.R;         // [R] place of the first fresh page in the ring; -1 = denied
-  int32_t* const s_back = s_first + p.R;        // [R] ended: place of its first returned page, counted from count; -1
+  int32_t* const s_ctx = plan_smem;          // [R]
+  int32_t* const s_new = s_ctx + p.R;        // [R] new tokens, then the place of the request's first
+                                             //     fresh page counted from the pool's head; -1 = denied
+  int32_t* const s_row = s_new + p.R;        // [R + 1] row starts, at most T
+  int32_t* const s_back = s_row + p.R + 1;   // [R + 1] first returned page, counted from the pool's count
   __shared__ long long warp_sums[PLAN_THREADS / 32];
   const int tid = threadIdx.x;
   const int page = 1 << p.page_shift;
@@ -81,30 +95,43 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
   pdl_wait();
   pdl_trigger();
   const int head_in = p.pool_in[0], count_in = p.pool_in[1];
+  for (int r = tid; r < p.R; r += PLAN_THREADS) {
+    s_ctx[r] = p.ctx_len[r];
+    s_new[r] = p.new_len[r];
+  }
   const bool pool_ok = head_in >= 0 && head_in < p.pages && count_in >= 0 && count_in <= p.pages;
   const int head = pool_ok ? head_in : 0, count = pool_ok ? count_in : 0;
   bool bad = !pool_ok;
+  __syncthreads();
 
   // This thread's requests: a contiguous run, so that its sums extend the block's.
   const int per = (p.R + PLAN_THREADS - 1) / PLAN_THREADS;
   const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
+  auto held = [&](int c) { return (int)((min(max((long long)c, 0LL), cap) + page - 1) >> p.page_shift); };
+  // Pages that a request with n > 0 new tokens, the last of them in row `end_row` - 1, begins; -1: no fit.
+  auto wanted = [&](int c, int n, long long end_row) {
+    const long long end = (long long)c + n;
+    if (c < 0 || end > cap || end_row > p.T) return -1;
+    return (int)((end + page - 1) >> p.page_shift) - held(c);
+  };
   long long rows = 0;
-  for (int r = r0; r < r1; ++r) rows += max(p.new_len[r], 0);
+  for (int r = r0; r < r1; ++r) rows += max(s_new[r], 0);
   long long all_rows, all_need, all_back;
   const long long row0 = block_exclusive_sum(rows, warp_sums, &all_rows);
 
   long long need = 0, back = 0, row = row0;
   for (int r = r0; r < r1; ++r) {
-    const int c = p.ctx_len[r], n = p.new_len[r];
-    s_ctx[r] = c;
+    const int c = s_ctx[r], n = s_new[r];
     s_row[r] = (int)min(row, (long long)p.T);
     row += max(n, 0);
-    const long long end = (long long)c + max(n, 0);
-    const bool fits = c >= 0 && end <= cap && (n <= 0 || row <= p.T);
-    if (!fits) bad = true;
-    const int have = (int)((min(max((long long)c, 0LL), cap) + page - 1) >> p.page_shift);
-    if (n > 0 && fits) need += ((end + page - 1) >> p.page_shift) - have;
-    if (n < 0) back += have;
+    if (c < 0 || c > cap) bad = true;
+    if (n > 0) {
+      const int w = wanted(c, n, row);
+      if (w < 0) bad = true;
+      need += max(w, 0);
+    } else if (n < 0) {
+      back += held(c);
+    }
   }
   const long long need0 = block_exclusive_sum(need, warp_sums, &all_need);
   const long long back0 = block_exclusive_sum(back, warp_sums, &all_back);
@@ -113,26 +140,31 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
   long long upto = need0, ret = back0, taken = 0, denied = 0;
   row = row0;
   for (int r = r0; r < r1; ++r) {
-    const int c = s_ctx[r], n = p.new_len[r];
+    const int c = s_ctx[r], n = s_new[r];
     row += max(n, 0);
-    const long long end = (long long)c + max(n, 0);
-    const bool fits = c >= 0 && end <= cap && row <= p.T;
-    const int have = (int)((min(max((long long)c, 0LL), cap) + page - 1) >> p.page_shift);
-    const long long want = n > 0 && fits ? ((end + page - 1) >> p.page_shift) - have : 0;
-    upto += want;
-    const bool granted = n > 0 && fits && (want == 0 || upto <= count);
-    s_first[r] = granted ? (int)(want ? upto - want : 0) : -1;
-    s_back[r] = n < 0 ? (int)min(ret, (long long)p.pages) : -1;
-    if (n < 0) ret += have;
-    if (granted) taken = max(taken, want ? upto : 0);
-    if (n > 0 && !granted) ++denied;
+    s_back[r] = (int)min(ret, (long long)p.pages);
+    bool granted = false;
+    if (n > 0) {
+      const int w = wanted(c, n, row);
+      upto += max(w, 0);
+      granted = w == 0 || (w > 0 && upto <= count);
+      s_new[r] = granted ? (int)(w ? upto - w : 0) : -1;
+      if (granted && w) taken = upto;
+      if (!granted) ++denied;
+    } else if (n < 0) {
+      ret += held(c);
+    }
     if (first_cta) {
       p.row_start[r] = s_row[r];
-      p.kv_len[r] = granted || n == 0 ? (int)end : 0;
-      p.next_ctx[r] = granted ? (int)end : n < 0 ? 0 : c;
+      p.kv_len[r] = granted ? c + n : n == 0 ? c : 0;
+      p.next_ctx[r] = granted ? c + n : n < 0 ? 0 : c;
     }
   }
-  if (tid == 0) s_row[p.R] = (int)min(all_rows, (long long)p.T);
+  const int used = (int)min(all_rows, (long long)p.T), returned = (int)min(all_back, (long long)p.pages);
+  if (tid == 0) {
+    s_row[p.R] = used;
+    s_back[p.R] = returned;
+  }
   if (first_cta) {
     // Sum of the denied and the largest granted sum of pages, over the block.
     long long all_denied;
@@ -143,40 +175,35 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
     if (taken) atomicMax(&s_taken, (int)taken);
     __syncthreads();
     if (tid == 0) {
-      const int gone = s_taken;
       // No more than `pages` pages are free: a caller that returns a page twice is told so.
-      const long long left = (long long)count - gone + all_back;
       if (count + all_back > p.pages) bad = true;
-      p.row_start[p.R] = (int)min(all_rows, (long long)p.T);
-      p.pool_out[0] = (int)(((long long)head + gone) % p.pages);
-      p.pool_out[1] = (int)min(left, (long long)p.pages);
-      p.info[0] = (int)min(all_rows, (long long)p.T);
-      p.info[1] = gone;
-      p.info[2] = (int)min(all_back, (long long)p.pages);
+      p.row_start[p.R] = used;
+      p.pool_out[0] = (int)(((long long)head + s_taken) % p.pages);
+      p.pool_out[1] = (int)min(count - s_taken + all_back, (long long)p.pages);
+      p.info[0] = used;
+      p.info[1] = s_taken;
+      p.info[2] = returned;
       p.info[3] = (int)all_denied;
     }
   }
   __syncthreads();
 
   // The rows' slots; a token at the first position of a page writes its table entry.
-  const int used = s_row[p.R];
+  auto ring = [&](int place) {  // place < 2 pages
+    const long long x = (long long)head + place;
+    return (int)(x >= p.pages ? x - p.pages : x);
+  };
   for (int t = blockIdx.x * PLAN_THREADS + tid; t < p.T; t += gridDim.x * PLAN_THREADS) {
     int slot = -1;
     if (t < used) {
-      int lo = 0, hi = p.R;  // the last r with s_row[r] <= t: s_row[lo] <= t < s_row[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_row[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      const int first = s_first[lo];
+      const int r = find_range(s_row, p.R, t), first = s_new[r];
       if (first >= 0) {
-        const int c = s_ctx[lo], pos = c + (t - s_row[lo]), j = pos >> p.page_shift;
+        const int c = s_ctx[r], pos = c + (t - s_row[r]), j = pos >> p.page_shift;
         const int have = (c + page - 1) >> p.page_shift;
-        int32_t* const entry = p.table + (long long)lo * p.max_pages + j;
+        int32_t* const entry = p.table + (long long)r * p.max_pages + j;
         int id;
         if (j >= have) {
-          id = p.pool[(int)(((long long)head + first + (j - have)) % p.pages)];
+          id = p.pool[ring(first + (j - have))];
           if ((pos & (page - 1)) == 0) *entry = id;
         } else {
           id = *entry;
@@ -187,18 +214,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
     }
     p.slot_map[t] = slot;
   }
-  // The ended requests' pages, one warp per request.
-  if (all_back) {
-    const int lane = tid % 32, warps = gridDim.x * (PLAN_THREADS / 32);
-    for (int r = blockIdx.x * (PLAN_THREADS / 32) + tid / 32; r < p.R; r += warps) {
-      const int b = s_back[r];
-      if (b < 0) continue;
-      const int have = (int)((min(max((long long)s_ctx[r], 0LL), cap) + page - 1) >> p.page_shift);
-      for (int j = lane; j < have; j += 32) {
-        const long long k = (long long)count + b + j;
-        if (k < p.pages) p.pool[(int)(((long long)head + k) % p.pages)] = p.table[(long long)r * p.max_pages + j];
-      }
-    }
+  // The ended requests' pages, behind the free ones.
+  for (int k = blockIdx.x * PLAN_THREADS + tid; k < returned && count + k < p.pages; k += gridDim.x * PLAN_THREADS) {
+    const int r = find_range(s_back, p.R, k);
+    p.pool[ring(count + k)] = p.table[(long long)r * p.max_pages + (k - s_back[r])];
   }
   if (bad) atomicOr(p.status, kDevCheck);
 }
@@ -220,38 +239,59 @@ struct AppendParams {
   float eps;
 };
 
-__global__ void paged_append_kernel(const AppendParams p) {
+// Half a warp per head, 16 bytes per lane; up to sixteen heads' loads are on their way before
+// the first reduction.  Bound by the memory system: 8192 rows of 8 + 2 + 2 heads move 50 MB.
+constexpr int APPEND_PAIRS = 8;
+__global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32, col = lane & 15, sub = lane >> 4;
   if (t >= p.T) return;
   const int heads = p.n_head + 2 * p.n_kv_head;
-  const uint2* src = reinterpret_cast<const uint2*>(p.qkv + (long long)t * heads * HD) + lane;
+  const uint4* src = reinterpret_cast<const uint4*>(p.qkv + (long long)t * heads * HD) + col;
   const int slot = p.slot_map[t];
   const bool kept = slot >= 0 && slot < p.slots;
-  const int page = kept ? slot >> p.page_shift : 0, off = slot & ((1 << p.page_shift) - 1);
-  for (int h = 0; h < heads; ++h) {
-    if (h >= p.n_head && !kept) break;
-    uint2 v = src[h * (HD / 4)];
-    if (h < p.n_head + p.n_kv_head) {
-      const float a = __uint_as_float(v.x << 16), b = __uint_as_float(v.x & 0xFFFF0000u);
-      const float c = __uint_as_float(v.y << 16), d = __uint_as_float(v.y & 0xFFFF0000u);
-      float ss = a * a + b * b + c * c + d * d;
+  const int last = kept ? heads : p.n_head;  // a row without a slot has its query heads alone moved
+  const long long page = kept ? slot >> p.page_shift : 0;
+  const int off = slot & ((1 << p.page_shift) - 1);
+  for (int h0 = 0; h0 < last; h0 += 2 * APPEND_PAIRS) {
+    uint4 v[APPEND_PAIRS];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
-      const float f = rsqrtf(ss * (1.0f / HD) + p.eps);
-      v = make_uint2(pack_bf16x2(a * f, b * f), pack_bf16x2(c * f, d * f));
+    for (int i = 0; i < APPEND_PAIRS; ++i) {
+      const int h = h0 + 2 * i + sub;
+      if (h < last) v[i] = src[h * (HD / 8)];
     }
-    uint16_t* dst;
-    if (h < p.n_head) {
-      dst = p.q + t * p.q_stride + h * HD;
-    } else {
-      const int g = (h - p.n_head) % p.n_kv_head;
-      const long long row = (((long long)page * p.n_kv_head + g) << p.page_shift) + off;
-      dst = (h < p.n_head + p.n_kv_head ? p.k_cache : p.v_cache) + row * HD;
+#pragma unroll
+    for (int i = 0; i < APPEND_PAIRS; ++i) {
+      const int h = h0 + 2 * i + sub;
+      if (h0 + 2 * i >= last) break;
+      uint32_t* const w = reinterpret_cast<uint32_t*>(&v[i]);
+      float f[8], ss = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        f[2 * x] = __uint_as_float(w[x] << 16);
+        f[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
+        ss += f[2 * x] * f[2 * x] + f[2 * x + 1] * f[2 * x + 1];
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
+      if (h >= last) continue;
+      if (h < p.n_head + p.n_kv_head) {
+        const float r = rsqrtf(ss * (1.0f / HD) + p.eps);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w[x] = pack_bf16x2(f[2 * x] * r, f[2 * x + 1] * r);
+      }
+      uint16_t* dst;
+      if (h < p.n_head) {
+        dst = p.q + t * p.q_stride + h * HD;
+      } else {
+        const bool key = h < p.n_head + p.n_kv_head;
+        const int g = h - p.n_head - (key ? 0 : p.n_kv_head);
+        dst = (key ? p.k_cache : p.v_cache) + (((page * p.n_kv_head + g) << p.page_shift) + off) * HD;
+      }
+      reinterpret_cast<uint4*>(dst)[col] = v[i];
     }
-    reinterpret_cast<uint2*>(dst)[lane] = v;
   }
 }
 
@@ -270,12 +310,16 @@ cudaError_t launch_paged_plan(const moe_paged_shape_t& s, const int32_t* ctx_len
   PlanParams p{ctx_len, new_len, block_table, pool, pool_in, pool_out, row_start, slot_map, kv_len, next_ctx, info,
                device_status_ptr(), s.requests, s.tokens, s.pages, s.max_pages, log2_of(s.page_size)};
   if (!p.status) return cudaErrorInvalidDevicePointer;
-  const size_t smem = sizeof(int32_t) * (4 * (size_t)s.requests + 1);
-  const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)(sizeof(int32_t) * (4 * kPagedMaxRequests + 1)));
-  if (e != cudaSuccess) return e;
-  const int blocks = (s.tokens + PLAN_THREADS - 1) / PLAN_THREADS;
-  return launch_pdl(paged_plan_kernel, dim3((unsigned)(blocks < 152 ? blocks : 152)), dim3(PLAN_THREADS), smem, st, p);
+  const size_t smem = sizeof(int32_t) * (4 * (size_t)s.requests + 2);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(sizeof(int32_t) * (4 * kPagedMaxRequests + 2)));
+    if (e != cudaSuccess) return e;
+  }
+  // Enough threads for the rows, and for an eighth of the tables' pages coming back at once.
+  const long long work = std::max<long long>(s.tokens, (long long)s.requests * s.max_pages / 8);
+  const long long blocks = std::min<long long>((work + PLAN_THREADS - 1) / PLAN_THREADS, 152);
+  return launch_pdl(paged_plan_kernel, dim3((unsigned)blocks), dim3(PLAN_THREADS), smem, st, p);
 }
 
 cudaError_t launch_paged_append(const moe_paged_shape_t& s, const uint16_t* qkv, const int32_t* slot_map, uint16_t* q,
