@@ -16,7 +16,7 @@
 // Work.  The unit is one 128-key tile of one work tile.  All units of the call, in order
 // (request, key/value head, query tile, key tile), are split into equal contiguous ranges, one
 // per CTA, whatever the requests' lengths (a work tile counts one unit more than it has key
-// tiles, for its query load and its output): a range holds the end of one work tile, whole work
+// tiles, a pair two, for its start and its output): a range holds the end of one work tile, whole work
 // tiles and the beginning of another.  A work tile that does not lie in one range leaves
 // partial outputs, which paged_combine_kernel joins in the order of the keys.  Every CTA
 // computes the ranges itself from the lengths (one prefix sum over the requests), so the call
@@ -134,30 +134,34 @@ __device__ __forceinline__ Request load_request(const PagedParams& p, int r, boo
   return q;
 }
 
-// Key tiles of the request's first k work tiles, all full (tQ = 2 tq tokens), and one unit
-// for each: tile i reaches position ctx + (i + 1) tQ.  With tQ dividing 128,
+// Key tiles of the request's first k work tiles, all full (tQ = 2 tq tokens: pairs), and two
+// units for each: tile i reaches position ctx + (i + 1) tQ.  With tQ dividing 128,
 // ceil((ctx + (i + 1) tQ) / 128) = ceil((c0 + i + 1) / P) for c0 = ceil(ctx / tQ) and
 // P = 128 / tQ, and the sum over i is a difference of sums of ceil(m / P); with tQ = 256 a
 // tile adds two key tiles to the last.
 __device__ __forceinline__ long long units_of_full(const Request& q, long long k, int tQ_shift) {
-  if (q.dead) return 2 * k;
-  if (tQ_shift > 7) return k * (k + 1) + k * ((q.ctx + BK - 1) >> 7) + k;
+  if (q.dead) return 3 * k;
+  if (tQ_shift > 7) return k * (k + 1) + k * ((q.ctx + BK - 1) >> 7) + 2 * k;
   const int ps = 7 - tQ_shift;
   const long long c0 = (q.ctx + (1 << tQ_shift) - 1) >> tQ_shift;
   auto sum = [ps](long long n) {
     const long long d = n >> ps, rem = n & ((1 << ps) - 1);
     return ((d * (d + 1)) >> 1 << ps) + rem * (d + 1);
   };
-  return sum(c0 + k) - sum(c0) + k;
+  return sum(c0 + k) - sum(c0) + 2 * k;
 }
 __device__ __forceinline__ int key_tiles(const Request& q, int i, int tQ_shift) {
   return q.dead ? 1 : (q.ctx + min(q.n, (i + 1) << tQ_shift) + BK - 1) >> 7;
 }
+// Units that work tile i counts beyond its key tiles: two with tokens in both halves.
+__device__ __forceinline__ int extra_units(const Request& q, int i, int tQ_shift) {
+  return q.n - (i << tQ_shift) > 1 << (tQ_shift - 1) ? 2 : 1;
+}
 // Units of one key/value head of the request.
 __device__ __forceinline__ long long head_units(const Request& q, int tQ_shift) {
   if (q.qn == 0) return 0;
-  if (q.qn == 1) return key_tiles(q, 0, tQ_shift) + 1;
-  return units_of_full(q, q.qn - 1, tQ_shift) + key_tiles(q, q.qn - 1, tQ_shift) + 1;
+  const int last = q.qn - 1, units = key_tiles(q, last, tQ_shift) + extra_units(q, last, tQ_shift);
+  return last == 0 ? units : units_of_full(q, last, tQ_shift) + units;
 }
 
 struct SmemState {
@@ -172,6 +176,7 @@ struct SmemState {
   long long warp_sum[WARPS];
   long long start_off;   // units of the starting request before the range
   int start_req;
+  Request start;
   uint32_t tmem;
 };
 static_assert(sizeof(SmemState) <= SMEM_BYTES - STATE_OFF, "the state fits behind the ring");
@@ -362,7 +367,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   const int per = (nreq + THREADS - 1) / THREADS;
   const int r0 = min(nreq, tid * per), r1 = min(nreq, r0 + per);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += head_units(load_request(p, r, blockIdx.x == 0), p.tQ_shift) * p.n_kv_head;
+  Request req{};  // the thread's last request: with up to 575 of them its only one
+  for (int r = r0; r < r1; ++r) {
+    req = load_request(p, r, blockIdx.x == 0);
+    mine += head_units(req, p.tQ_shift) * p.n_kv_head;
+  }
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -387,15 +396,19 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   const long long u1 = !working ? 0 : one ? c + 1 : div_ll(total * (c + 1), ctas);
   if (working && mine > 0 && u0 >= upto - mine && u0 < upto) {
     long long at = upto - mine;
-    for (int r = r0; r < r1; ++r) {
-      const long long w = head_units(load_request(p, r, false), p.tQ_shift) * p.n_kv_head;
-      if (u0 < at + w) {
-        sm.start_req = r;
-        sm.start_off = u0 - at;
-        break;
+    int r = r0;
+    if (per > 1) {
+      while (true) {
+        req = load_request(p, r, false);
+        const long long units = head_units(req, p.tQ_shift) * p.n_kv_head;
+        if (u0 < at + units) break;
+        at += units;
+        ++r;
       }
-      at += w;
     }
+    sm.start = req;
+    sm.start_req = r;
+    sm.start_off = u0 - at;
   }
   __syncthreads();
   const uint32_t tmem = sm.tmem;
@@ -410,15 +423,16 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     const int rows_end = (int)((long long)p.pages * p.n_kv_head << p.page_shift);  // out of range: zeros
     int r = working ? sm.start_req : 0;
     long long off = working ? sm.start_off : 0;
-    Request q{};
+    Request q = sm.start;
     int g = 0;
     int i = 0;  // the work tile that holds unit `off` of the head: units_of_full(i) <= off
     if (working) {
-      q = load_request(p, r, false);
-      const long long units = head_units(q, p.tQ_shift);
-      while (off >= units) {
-        off -= units;
-        ++g;
+      if (p.n_kv_head > 1) {
+        const long long units = head_units(q, p.tQ_shift);
+        while (off >= units) {
+          off -= units;
+          ++g;
+        }
       }
       int hi = q.qn;
       while (hi - i > 1) {
@@ -435,17 +449,17 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     bool ok = true;
     while (ok && unit < u1) {
       const int tile_n = key_tiles(q, i, p.tQ_shift);
-      const int units = (int)min((long long)(tile_n + 1 - j), u1 - unit);  // of this work tile in the range
+      const int units = (int)min((long long)(tile_n + extra_units(q, i, p.tQ_shift) - j), u1 - unit);  // in the range
       Item it;
       it.row0 = q.row0 + (i << p.tQ_shift);
       it.ntok = min(1 << p.tQ_shift, q.n - (i << p.tQ_shift));
       it.pos0 = q.ctx + (i << p.tQ_shift);
       it.kvlim = q.dead ? 0 : it.pos0 + it.ntok;
       it.j0 = j;
-      it.nt = min(units, tile_n - j);  // the unit past the key tiles holds no work
+      it.nt = min(units, tile_n - j);  // the units past the key tiles hold no work
       it.g = g;
       if (it.nt > 0) {
-        // Page ids of the first key tile, on their way while the item is published.
+        // Page ids of the first key tile.
         const int32_t* const row = p.table + (long long)r * p.max_pages;
         auto page_id = [&](int t) {  // -1: no key there that the tile may see
           const int page = (it.j0 + t) * nb + box;
@@ -455,16 +469,22 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         it.half = it.ntok > p.tq ? 2 : next_half;
         const bool ends = j + it.nt == tile_n;
         it.part = j == 0 && ends ? -1 : (j == 0 ? 2 * c + 1 : 2 * c);
-        const int slot = items % ITEMS;
-        if (!warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status)) break;
-        if (lane == 0) {
-          sm.items[slot] = it;
-          mbar_arrive(smem_u32(&sm.item_full[slot]));
+        // The query halves, while the page ids are on their way.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || (it.half != 2 && it.half != h)) continue;
+          ok = warp_wait(&sm.q_empty[h], q_uses[h] ^ 1u, p.status);
+          if (!ok) continue;
+          if (lane == 0) {
+            const uint32_t qbar = smem_u32(&sm.q_full[h]);
+            mbar_arrive_expect_tx(qbar, q_bytes);
+            const int tok = it.row0 + (it.half == 2 ? h * p.tq : 0);
+            tma_load_4d(base + h * TILE_BYTES, &p.q, qbar, 0, 0, g * p.G, tok);
+            tma_load_4d(base + h * TILE_BYTES + ATOM_BYTES, &p.q, qbar, 0, 1, g * p.G, tok);
+          }
+          ++q_uses[h];
         }
-        __syncwarp();
-        ++items;
-        // The key and value tiles, one box per page and column half and lane; the query halves
-        // behind the first key tile.
+        // The key and value tiles, one box per page and column half and lane.
         for (int t = 0; t < it.nt && ok; ++t) {
           const bool there = ((long long)((it.j0 + t) * nb + box) << p.page_shift) < it.kvlim;
           int coord = rows_end;
@@ -486,22 +506,16 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             if (copies)
               tma_load_3d(base + RING_OFF + st * TILE_BYTES + box_dst, kv ? &p.v : &p.k, bar, 0, coord, col);
             ++loads;
-            if (t == 0 && kv == 0) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (!ok || (it.half != 2 && it.half != h)) continue;
-                ok = warp_wait(&sm.q_empty[h], q_uses[h] ^ 1u, p.status);
-                if (!ok) continue;
-                if (lane == 0) {
-                  const uint32_t qbar = smem_u32(&sm.q_full[h]);
-                  mbar_arrive_expect_tx(qbar, q_bytes);
-                  const int tok = it.row0 + (it.half == 2 ? h * p.tq : 0);
-                  tma_load_4d(base + h * TILE_BYTES, &p.q, qbar, 0, 0, g * p.G, tok);
-                  tma_load_4d(base + h * TILE_BYTES + ATOM_BYTES, &p.q, qbar, 0, 1, g * p.G, tok);
-                }
-                ++q_uses[h];
-              }
+            if (t == 0 && kv == 0) {  // the item, behind its first key tile
+              const int slot = items % ITEMS;
+              ok = warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status);
               if (!ok) break;
+              if (lane == 0) {
+                sm.items[slot] = it;
+                mbar_arrive(smem_u32(&sm.item_full[slot]));
+              }
+              __syncwarp();
+              ++items;
             }
           }
         }
@@ -830,27 +844,23 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       // ---- the item's output: O / l, or the partial
       l[0] = quad_sum(l[0]);
       l[1] = quad_sum(l[1]);
+      float inv[2];
+      uint16_t* dst[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        inv[x] = l[x] > 0.f ? 1.0f / l[x] : 0.f;
+        const int mr = lane0 + lane / 4 + 8 * x, tok_in = mr / p.G;
+        const long long row = (long long)(it.row0 + (pair ? wg * p.tq : 0) + tok_in) * p.n_head + it.g * p.G +
+                              (mr - tok_in * p.G);
+        dst[x] = p.out + row * HD + quad * 8;
+        if (it.part < 0 && (valid >> x & 1) && p.lse && quad == 0)
+          p.lse[row] = l[x] > 0.f ? (m[x] + log2f(l[x])) * LN2 : -INFINITY;
+      }
       if (!half_wait(&sm.o_full[wg], outs++, wg, p.status)) break;
       tc_fence_after();
       if (active) {
         if (it.part < 0) {
-          float inv[2];
-          uint16_t* dst[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            inv[x] = l[x] > 0.f ? 1.0f / l[x] : 0.f;
-            const int mr = lane0 + lane / 4 + 8 * x, tok_in = mr / p.G;
-            const long long row = (long long)(it.row0 + (pair ? wg * p.tq : 0) + tok_in) * p.n_head + it.g * p.G +
-                                  (mr - tok_in * p.G);
-            dst[x] = p.out + row * HD + quad * 8;
-            if ((valid >> x & 1) && p.lse && quad == 0)
-              p.lse[row] = l[x] > 0.f ? (m[x] + log2f(l[x])) * LN2 : -INFINITY;
-          }
-#pragma unroll 1
-          for (int y = 0; y < HD / 32; ++y) {  // 32 columns: four groups of eight
-            uint32_t o[16];
-            tmem_ld_quad4(ocol + 32 * y, o);
-            tmem_wait_quad4(o);
+          auto store = [&](const uint32_t(&o)[16], int y) {  // 32 columns: four groups of eight
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               uint32_t w[4];
@@ -874,6 +884,17 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               const uint4 line = quad & 2 ? make_uint4(a2, a3, a0, a1) : make_uint4(a0, a1, a2, a3);
               if (valid >> x & 1) *reinterpret_cast<uint4*>(dst[x] + y * 32) = line;
             }
+          };
+          uint32_t oa[16], ob[16];  // the next columns load while these are stored
+          tmem_ld_quad4(ocol, oa);
+#pragma unroll
+          for (int y = 0; y < HD / 32; y += 2) {
+            tmem_wait_quad4(oa);
+            tmem_ld_quad4(ocol + 32 * (y + 1), ob);
+            store(oa, y);
+            tmem_wait_quad4(ob);
+            if (y + 2 < HD / 32) tmem_ld_quad4(ocol + 32 * (y + 2), oa);
+            store(ob, y + 1);
           }
         } else {
           uint8_t* const part = p.parts + (size_t)it.part * PART_BYTES;
