@@ -18,7 +18,10 @@
 // per CTA, whatever the requests' lengths (a work tile counts one unit more than it has key
 // tiles, a pair two, for its start and its output): a range holds the end of one work tile, whole work
 // tiles and the beginning of another.  A work tile that does not lie in one range leaves
-// partial outputs, which paged_combine_kernel joins in the order of the keys.  Every CTA
+// partial outputs.  A pair's first part is the last work of its range and the others the first
+// work of theirs, written long since: with up to three of them the CTA of the first part adds
+// them to its own sums.  Other joins (few rows, or many parts) are paged_combine_kernel's,
+// eight blocks to a tile.  Either way in the order of the keys.  Every CTA
 // computes the ranges itself from the lengths (one prefix sum over the requests), so the call
 // needs no plan, no counters and no cleared workspace.  Rows that belong to no request are the
 // rows of one more request without keys; their units read nothing and give zeros.
@@ -41,6 +44,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+#include <chrono>
 #include <cstring>
 
 #include "internal.h"
@@ -74,11 +79,16 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr size_t PART_O = 16 * 256 * 32;
 constexpr size_t PART_BYTES = PART_O + 2 * 256 * 4;
 
-// One work tile that goes on past the range of the CTA that begins it.
+// A part that another CTA adds has a flag per warp that writes it, the call's id once it is
+// written; who adds it clears the flag.  Any other value means not written, so the workspace
+// needs no clearing.
+constexpr int MOST_ADDED = 2;
+constexpr size_t FLAG_BYTES = CTAS * SOFTMAX_WARPS * sizeof(unsigned long long);
+// A work tile that paged_combine_kernel joins, by the CTA that begins it.
 struct Split {
   int row0, ntok, g, last;  // first token row, tokens, key/value head, last CTA with a part (-1: none)
 };
-constexpr size_t SCRATCH_BYTES = CTAS * sizeof(Split) + 2 * CTAS * PART_BYTES;
+constexpr size_t SCRATCH_BYTES = FLAG_BYTES + CTAS * sizeof(Split) + 2 * CTAS * PART_BYTES;
 
 struct PagedParams {
   CUtensorMap q;  // [T] rows viewed as (64, 2, n_head, T), box (64, 1, G, tq)
@@ -89,6 +99,8 @@ struct PagedParams {
   const int32_t* kv_len;
   uint16_t* out;
   float* lse;
+  unsigned long long* flags;  // [CTA][softmax warp]
+  unsigned long long call;    // this call's id
   Split* splits;
   uint8_t* parts;
   int* status;
@@ -102,7 +114,8 @@ struct Item {
   int kvlim;        // keys that its last token sees; 0 = a request without keys
   int j0, nt;       // first key tile, key tiles of this item; nt == 0 ends the walk
   int g, half;      // key/value head; query half of a single tile, 2 = pair
-  int part;         // -1 = the whole work tile, else the partial slot
+  int part;         // partial slot to write; -1 = none: the whole work tile, or the part that adds the others
+  int added;        // parts that the first CTA adds to its own; 0 = none
 };
 
 // One request's work tiles.
@@ -321,6 +334,64 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(FULL, x, 2);
 }
 
+// Adds another CTA's part of the warp's sixteen rows to the warp's own: O in TMEM, m and l.
+// The same rows are the same warp's in every CTA, so a warp waits for a warp.  Bounded; on a
+// timeout the status word is set and the warp goes on (its output is then unspecified).
+__device__ __forceinline__ void add_part(const uint8_t* part, unsigned long long* flag, unsigned long long call,
+                                         int* status, int prow, uint32_t valid, uint32_t ocol, float (&m)[2],
+                                         float (&l)[2]) {
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) {
+    unsigned long long t0 = 0, v;
+    while (true) {
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
+      if (v == call) break;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        atomicOr(status, kDevTimeout);
+        break;
+      }
+      __nanosleep(64);
+    }
+    *flag = 0;
+  }
+  __syncwarp();
+  __threadfence();
+  const float* const ml = reinterpret_cast<const float*>(part + PART_O) + prow;
+  const float2* const po = reinterpret_cast<const float2*>(part) + prow * 4 + (lane & 3);
+  float f[2], w[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const bool in = valid >> x & 1;
+    const float mo = in ? __ldcg(ml + 8 * x) : -INFINITY, lo = in ? __ldcg(ml + 256 + 8 * x) : 0.f;
+    const float top = fmaxf(m[x], mo);
+    f[x] = m[x] == top ? 1.f : ex2(m[x] - top);
+    w[x] = mo == -INFINITY ? 0.f : ex2(mo - top);
+    m[x] = top;
+    l[x] = f[x] * l[x] + w[x] * lo;
+  }
+#pragma unroll 1
+  for (int y = 0; y < HD / 32; ++y) {
+    uint32_t o[16];
+    tmem_ld_quad4(ocol + 32 * y, o);
+    float2 v[8];  // a weight of 0 (a row without keys in that part) hides what it holds
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = w[k & 1] != 0.f ? __ldcg(po + (y * 4 + (k >> 1)) * 1024 + (k & 1) * 32) : make_float2(0.f, 0.f);
+    tmem_wait_quad4(o);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float g = f[k & 1], h = w[k & 1];
+      o[2 * k] = __float_as_uint(fmaf(h, v[k].x, g != 0.f ? g * __uint_as_float(o[2 * k]) : 0.f));
+      o[2 * k + 1] = __float_as_uint(fmaf(h, v[k].y, g != 0.f ? g * __uint_as_float(o[2 * k + 1]) : 0.f));
+    }
+    tmem_st_quad4(ocol + 32 * y, o);
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   SmemState& sm = *reinterpret_cast<SmemState*>(smem + STATE_OFF);
@@ -468,7 +539,15 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         int id = page_id(0);
         it.half = it.ntok > p.tq ? 2 : next_half;
         const bool ends = j + it.nt == tile_n;
-        it.part = j == 0 && ends ? -1 : (j == 0 ? 2 * c + 1 : 2 * c);
+        it.part = -1;
+        it.added = 0;
+        if (j > 0 || !ends) {  // unit u belongs to CTA ((u + 1) ctas - 1) / total
+          const int cf = j == 0 ? c : (int)div_ll((unit - j + 1) * ctas - 1, total);
+          const int cl = ends ? c : (int)div_ll((unit - j + tile_n) * ctas - 1, total);
+          if (cl - cf <= (it.half == 2 ? MOST_ADDED : 0)) it.added = cl - cf;
+          if (j > 0 || it.added == 0) it.part = j == 0 ? 2 * c + 1 : 2 * c;
+          if (j == 0 && it.added == 0) split = Split{it.row0, it.ntok, g, cl};
+        }
         // The query halves, while the page ids are on their way.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -520,8 +599,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           }
         }
         if (it.half != 2) next_half = it.half ^ 1;
-        // Unit u belongs to CTA ((u + 1) ctas - 1) / total: the tile's last key tile.
-        if (j == 0 && !ends) split = Split{it.row0, it.ntok, g, (int)div_ll((unit + tile_n) * ctas - 1, total)};
       }
       unit += units;
       // The next work tile: query tile, then head, then request.
@@ -635,27 +712,44 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         score(half, 0, key.stage);
         commit(&sm.s_full[2]);
         commit(&sm.ring_empty[key.stage]);
+        if (nt == 1) commit(&sm.q_empty[half]);
         for (int t = 0; t < nt; ++t) {
+          // The score product of the next tile and this tile's value product, whichever can go
+          // first: a late key tile does not keep the value tile's stage.
           const int b = t & 1;
           const Ring val = key.next(), next = val.next();
-          if (t + 1 < nt) {
-            ok = mbar_wait_all(full(next), next.phase, full(next), next.phase, full(next), next.phase, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            score(half, b ^ 1, next.stage);
-            commit(&sm.s_full[2 + (b ^ 1)]);
-            commit(&sm.ring_empty[next.stage]);
-          } else {
-            commit(&sm.q_empty[half]);  // every score product is issued
-          }
           const uint32_t pf = smem_u32(&sm.p_full[2 + b]), pp = ((b ? odd : even) + (t >> 1)) & 1u;
-          ok = mbar_wait_all(pf, pp, full(val), val.phase, pf, pp, p.status);
+          bool scored = t + 1 == nt, valued = false;
+          unsigned long long t0 = 0;
+          for (uint32_t polls = 1; !(scored && valued); ++polls) {
+            if (!scored && mbar_test_all(full(next), next.phase, full(next), next.phase, full(next), next.phase)) {
+              tc_fence_after();
+              score(half, b ^ 1, next.stage);
+              commit(&sm.s_full[2 + (b ^ 1)]);
+              commit(&sm.ring_empty[next.stage]);
+              if (t + 2 == nt) commit(&sm.q_empty[half]);  // every score product is issued
+              scored = true;
+            }
+            if (!valued && mbar_test_all(pf, pp, full(val), val.phase, pf, pp)) {
+              tc_fence_after();
+              value(0, b, val.stage, t == 0);
+              if (t + 1 == nt) commit(&sm.o_full[0]);
+              commit(&sm.pv_done[b]);
+              commit(&sm.ring_empty[val.stage]);
+              valued = true;
+            }
+            if (polls % 256 == 0) {  // bounded as every wait
+              const unsigned long long now = globaltimer_ns();
+              if (t0 == 0) {
+                t0 = now;
+              } else if (now - t0 > kWaitLimitNs) {
+                if (issues) atomicOr(p.status, kDevTimeout);
+                ok = false;
+                break;
+              }
+            }
+          }
           if (!ok) break;
-          tc_fence_after();
-          value(0, b, val.stage, t == 0);
-          if (t + 1 == nt) commit(&sm.o_full[0]);
-          commit(&sm.pv_done[b]);
-          commit(&sm.ring_empty[val.stage]);
           key = next;
         }
         even += (nt + 1) >> 1;
@@ -844,6 +938,16 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       // ---- the item's output: O / l, or the partial
       l[0] = quad_sum(l[0]);
       l[1] = quad_sum(l[1]);
+      const bool adds = it.added && it.part < 0;
+      if (__builtin_expect(adds, 0)) {
+        if (!half_wait(&sm.o_full[wg], outs, wg, p.status)) break;
+        tc_fence_after();
+        if (active)
+          for (int i = 1; i <= it.added; ++i)
+            add_part(p.parts + (size_t)(2 * (blockIdx.x + i)) * PART_BYTES,
+                     p.flags + (blockIdx.x + i) * SOFTMAX_WARPS + warp, p.call, p.status,
+                     (pair ? wg * 128 : 0) + lane0 + lane / 4, valid, ocol, m, l);
+      }
       float inv[2];
       uint16_t* dst[2];
 #pragma unroll
@@ -856,7 +960,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (it.part < 0 && (valid >> x & 1) && p.lse && quad == 0)
           p.lse[row] = l[x] > 0.f ? (m[x] + log2f(l[x])) * LN2 : -INFINITY;
       }
-      if (!half_wait(&sm.o_full[wg], outs++, wg, p.status)) break;
+      if (!adds && !half_wait(&sm.o_full[wg], outs, wg, p.status)) break;
+      ++outs;
       tc_fence_after();
       if (active) {
         if (it.part < 0) {
@@ -918,6 +1023,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               ml[8 * x] = m[x];
               ml[256 + 8 * x] = l[x];
             }
+          if (it.added) {
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) atomicExch(p.flags + blockIdx.x * SOFTMAX_WARPS + warp, p.call);
+          }
         }
       }
       __syncwarp();
@@ -1088,8 +1198,14 @@ cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q
   p.kv_len = kv_len;
   p.out = out;
   p.lse = lse;
-  p.splits = static_cast<Split*>(scratch);
-  p.parts = static_cast<uint8_t*>(scratch) + CTAS * sizeof(Split);
+  p.flags = static_cast<unsigned long long*>(scratch);
+  p.splits = reinterpret_cast<Split*>(static_cast<uint8_t*>(scratch) + FLAG_BYTES);
+  p.parts = static_cast<uint8_t*>(scratch) + FLAG_BYTES + CTAS * sizeof(Split);
+  // An id for every call of the process, from a start that a flag does not hold by chance.  A
+  // replay of a captured call has the capture's id and finds the flags cleared.
+  static std::atomic<unsigned long long> calls{
+      (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() << 20 | 1u};
+  p.call = calls.fetch_add(1);
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInvalidDevicePointer;
   p.R = s.requests;

@@ -278,7 +278,7 @@ def _check_attention(a, scale=1.0, **kw):
         assert np.array_equal(np.isneginf(ls), empty)
         keys = int(a["kv"].max())
         tol = ds + 2.0 ** -24 * keys + 2.0 ** -20 * (1 + np.abs(ref["lse"]))
-        assert (np.abs(ls - ref["lse"])[~empty] <= tol[~empty]).all()
+        assert (np.abs(ls[~empty] - ref["lse"][~empty]) <= tol[~empty]).all()
     # Rows without keys are exactly zero.
     assert (got.reshape(T, a["H"], 128)[np.isneginf(ref["lse"])] == 0).all()
 
@@ -306,6 +306,15 @@ ATTN = {
     "one-head": ([300], [150], 1, 1, 128, 2),
     "mixed-step": ([700, 0, 64, 1, 2000, 0], [1, 180, 1, 40, 1, 1], 8, 2, 16, 40),
     "idle-requests-between": ([100, 50, 7, 0, 90], [1, 0, 3, 0, 1], 8, 2, 16, 2),
+    # Work tiles in one, two, three and many parts over the CTAs, pairs and single ones.
+    "prompt-2048": ([0], [2048], 8, 2, 64, 0),
+    "chunk-in-many-parts": ([20000], [64], 8, 2, 32, 1),
+    "chunks-in-three-parts": ([6000, 5000], [700, 27], 4, 1, 128, 0),
+    "few-rows-in-many-parts": ([9000, 9100], [3, 5], 8, 2, 64, 0),
+    # More requests than the kernel has threads.
+    "decode-700": ([int(x) for x in np.random.default_rng(1).integers(0, 70, 700)], [1] * 700, 4, 1, 16, 0),
+    "decode-1300-some-idle": ([int(x) for x in np.random.default_rng(2).integers(0, 40, 1300)],
+                              [int(x) for x in np.random.default_rng(3).integers(0, 3, 1300)], 2, 2, 16, 50),
 }
 
 
@@ -382,6 +391,55 @@ def test_attention_far_into_a_large_cache():
     torch.cuda.synchronize()
     st = torch.tensor(slots, device=DEV)
     assert torch.equal(v[st // page, :, st % page].reshape(T, -1), qkv[:, 10 * 128:])
+
+
+def test_attention_through_one_workspace_and_a_captured_graph():
+    """Calls of other lengths through one workspace, directly and as replays of one captured
+    call whose lengths change: equal bits.  What a call leaves in the workspace, and where its
+    work tiles are cut, differ from call to call."""
+    rng = np.random.default_rng(16)
+    H, KV, page, T = 8, 2, 16, 1300
+    steps = [([0, 3000, 700, 1], [1200, 1, 60, 39]), ([9000, 10, 10, 10], [64, 1, 1, 1]), ([0, 0, 0, 0], [1, 1, 1, 1]),
+             ([100, 200, 5000, 300], [300, 500, 400, 100]), ([2500, 2600, 2700, 2800], [325, 325, 325, 325])]
+    ins = [_attn_inputs(rng, c, n, H, KV, page, pad=T - sum(n)) for c, n in steps]
+    pages, width = max(a["pages"] for a in ins), max(a["table"].shape[1] for a in ins)
+    shape = M.make_paged_shape(4, T, H, KV, page, pages, width)
+    ws = torch.randint(0, 256, (M.moe_paged_attention_workspace_size(shape),), dtype=torch.uint8, device=DEV)
+    k = torch.empty(pages, KV, page, 128, dtype=torch.bfloat16, device=DEV)
+    v, q = torch.empty_like(k), torch.empty(T, H * 128, dtype=torch.bfloat16, device=DEV)
+    table, rs, kv = torch.empty(4, width, dtype=torch.int32, device=DEV), _i32([0] * 5), _i32([0] * 4)
+    out, lse = torch.empty_like(q), torch.empty(T, H, dtype=torch.float32, device=DEV)
+
+    def load(a):
+        k[:a["pages"]], v[:a["pages"]] = a["k"], a["v"]
+        q.copy_(a["q"])
+        table.fill_(-1)
+        table[:, :a["table"].shape[1]] = _i32(a["table"])
+        rs.copy_(_i32(a["row_start"]))
+        kv.copy_(_i32(a["kv"]))
+
+    def call(stream=None):
+        M.moe_paged_attention(shape, q, k, v, table, rs, kv, out, lse, ws, stream=stream)
+
+    direct = []
+    for a in ins:
+        load(a)
+        call()
+        torch.cuda.synchronize()
+        direct.append((out.clone(), lse.clone()))
+        ref, ref_lse = _attend(a)  # a workspace of its own
+        assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(lse, ref_lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(side)
+    for i in (0, 1, 3, 0, 4, 2, 4, 1, 0):
+        load(ins[i])
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), direct[i][0].view(torch.int16)) and torch.equal(lse, direct[i][1])
 
 
 def test_attention_reports_tables_and_lengths_out_of_range():
