@@ -28,8 +28,8 @@
 //
 // paged_attention_kernel, one CTA per SM, 18 warps:
 //   - warp 16 walks the CTA's range, publishes each item (work tile, key tiles) in a small
-//     ring, and issues the TMA copies: the query halves, and one box per page and 64-column
-//     half of the key and value tiles, into a ring of five 32 KB stages;
+//     ring, and issues the TMA copies: the query halves, and one box per page of the key and
+//     value tiles, into a ring of five 32 KB stages;
 //   - warp 17 (one thread) issues tcgen05.mma: S = Q K^T into a score buffer, O += P V with P
 //     (bf16) read from the score buffer's own columns.  The pipe runs in order, so a score
 //     product that overwrites a buffer needs no wait for the product that read P from it;
@@ -92,7 +92,7 @@ constexpr size_t SCRATCH_BYTES = FLAG_BYTES + CTAS * sizeof(Split) + 2 * CTAS * 
 
 struct PagedParams {
   CUtensorMap q;  // [T] rows viewed as (64, 2, n_head, T), box (64, 1, G, tq)
-  CUtensorMap k;  // cache viewed as (64, rows, 2), box (64, page, 1)
+  CUtensorMap k;  // cache viewed as (64, 8, 2, rows / 8): groups of eight rows, their two column halves; box a page
   CUtensorMap v;
   const int32_t* table;
   const int32_t* row_start;
@@ -175,6 +175,16 @@ __device__ __forceinline__ long long head_units(const Request& q, int tQ_shift) 
   if (q.qn == 0) return 0;
   const int last = q.qn - 1, units = key_tiles(q, last, tQ_shift) + extra_units(q, last, tQ_shift);
   return last == 0 ? units : units_of_full(q, last, tQ_shift) + units;
+}
+
+// Descriptor of a key or value tile in shared memory: [16 groups][2 halves][8 rows][64] bf16,
+// 128-byte swizzle, as one box per page lays it down whatever the page's size.  A group of eight
+// keys and the next are 2048 bytes apart (the stride byte offset: along N for the keys, which are
+// K-major, along K for the values, which are MN-major), a half and the other 1024 (the leading
+// byte offset of the values' 64-column atoms).
+__device__ __forceinline__ uint64_t kv_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1024 >> 4) << 16 |
+         static_cast<uint64_t>(2048 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
 }
 
 struct SmemState {
@@ -487,11 +497,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   if (warp == LOAD_WARP) {
     // ------------------------------------------------------------ walk and TMA copies
     const int nb = BK >> p.page_shift;         // pages per key tile
-    const int box = lane & (nb - 1), col = lane >= nb ? 1 : 0;
-    const bool copies = lane < 2 * nb;
-    const uint32_t box_dst = col * ATOM_BYTES + (box << p.page_shift) * 128;
+    const int box = lane & (nb - 1);
+    const bool copies = lane < nb;
+    const uint32_t box_dst = (box << p.page_shift) * 256;
     const uint32_t q_bytes = (uint32_t)(2 * p.tq * p.G * 128);
-    const int rows_end = (int)((long long)p.pages * p.n_kv_head << p.page_shift);  // out of range: zeros
+    const int rows_end = (int)(((long long)p.pages * p.n_kv_head << p.page_shift) >> 3);  // out of range: zeros
     int r = working ? sm.start_req : 0;
     long long off = working ? sm.start_off : 0;
     Request q = sm.start;
@@ -563,12 +573,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           }
           ++q_uses[h];
         }
-        // The key and value tiles, one box per page and column half and lane.
+        // The key and value tiles, one box per page and lane.
         for (int t = 0; t < it.nt && ok; ++t) {
           const bool there = ((long long)((it.j0 + t) * nb + box) << p.page_shift) < it.kvlim;
           int coord = rows_end;
           if (copies && there) {
-            if (id >= 0 && id < p.pages) coord = (id * p.n_kv_head + g) << p.page_shift;
+            if (id >= 0 && id < p.pages) coord = (id * p.n_kv_head + g) << (p.page_shift - 3);
             else atomicOr(p.status, kDevCheck);
           }
           if (t + 1 < it.nt) id = page_id(t + 1);
@@ -583,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             if (lane == 0) mbar_arrive_expect_tx(bar, TILE_BYTES);
             __syncwarp();
             if (copies)
-              tma_load_3d(base + RING_OFF + st * TILE_BYTES + box_dst, kv ? &p.v : &p.k, bar, 0, coord, col);
+              tma_load_4d(base + RING_OFF + st * TILE_BYTES + box_dst, kv ? &p.v : &p.k, bar, 0, 0, 0, coord);
             ++loads;
             if (t == 0 && kv == 0) {  // the item, behind its first key tile
               const int slot = items % ITEMS;
@@ -641,21 +651,21 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     Ring key{0, 0};  // of the next key tile; its value tile is the stage behind
     auto score = [&](int half, int buf, uint32_t st) {  // S[buf] = Q[half] K^T
       const uint64_t qd = sw128_kmajor_desc(base + half * TILE_BYTES);
-      const uint64_t kd = sw128_kmajor_desc(base + RING_OFF + st * TILE_BYTES);
+      const uint64_t kd = kv_desc(base + RING_OFF + st * TILE_BYTES);
       if (issues) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           tc_mma_bf16(tmem + buf * BK, qd + (kk >> 2) * (ATOM_BYTES >> 4) + 2 * (kk & 3),
-                      kd + (kk >> 2) * (ATOM_BYTES >> 4) + 2 * (kk & 3), id_s, kk != 0);
+                      kd + (kk >> 2) * (1024 >> 4) + 2 * (kk & 3), id_s, kk != 0);
       }
     };
     auto value = [&](int out, int buf, uint32_t st, bool first) {  // O[out] (+)= P[buf] V
-      const uint64_t vd = sw128_mnmajor_desc(base + RING_OFF + st * TILE_BYTES, ATOM_BYTES);
+      const uint64_t vd = kv_desc(base + RING_OFF + st * TILE_BYTES);
       if (issues) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
           tc_mma_bf16_a_tmem(tmem + O_COL + out * HD, tmem + buf * BK + (kk >> 2) * 64 + (kk & 3) * 8,
-                             vd + kk * 128u, id_pv, !first || kk != 0);
+                             vd + kk * 256u, id_pv, !first || kk != 0);
       }
     };
     auto commit = [&](const uint64_t* bar) {
@@ -814,8 +824,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           }
           const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
           if (zrow >= kvlim - k0) {
-            uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + zcol * ATOM_BYTES +
-                                                      zrow * 128);
+            uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + (zrow >> 3) * 2048 +
+                                                      zcol * 1024 + (zrow & 7) * 128);
 #pragma unroll
             for (int x = 0; x < 8; ++x) z[x] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
@@ -1188,10 +1198,10 @@ cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q
   const uint64_t qstrides[3] = {128, 256, (uint64_t)q_stride * 2};
   const uint32_t qbox[4] = {64, 1, (uint32_t)p.G, (uint32_t)p.tq};
   const uint64_t rows = (uint64_t)s.pages * s.n_kv_head * s.page_size;
-  const uint64_t kdims[3] = {64, rows, 2}, kstrides[2] = {256, 128};
-  const uint32_t kbox[3] = {64, (uint32_t)s.page_size, 1};
-  if (!encode_tma_bf16(&p.q, q, 4, qdims, qstrides, qbox) || !encode_tma_bf16(&p.k, k_cache, 3, kdims, kstrides, kbox) ||
-      !encode_tma_bf16(&p.v, v_cache, 3, kdims, kstrides, kbox))
+  const uint64_t kdims[4] = {64, 8, 2, rows / 8}, kstrides[3] = {256, 128, 2048};
+  const uint32_t kbox[4] = {64, 8, 2, (uint32_t)s.page_size / 8};
+  if (!encode_tma_bf16(&p.q, q, 4, qdims, qstrides, qbox) || !encode_tma_bf16(&p.k, k_cache, 4, kdims, kstrides, kbox) ||
+      !encode_tma_bf16(&p.v, v_cache, 4, kdims, kstrides, kbox))
     return cudaErrorInvalidValue;
   p.table = block_table;
   p.row_start = row_start;
