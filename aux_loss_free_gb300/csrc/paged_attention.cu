@@ -46,6 +46,7 @@
 
 #include <atomic>
 #include <chrono>
+#include <cstddef>
 #include <cstring>
 
 #include "internal.h"
@@ -188,6 +189,7 @@ __device__ __forceinline__ uint64_t kv_desc(uint32_t addr) {
 }
 
 struct SmemState {
+  // Barriers, one array after the other.
   uint64_t q_full[2], q_empty[2];
   uint64_t ring_full[STAGES], ring_empty[STAGES];
   uint64_t s_full[4];    // pair: half 0, 1; single: even, odd key tile
@@ -203,6 +205,8 @@ struct SmemState {
   uint32_t tmem;
 };
 static_assert(sizeof(SmemState) <= SMEM_BYTES - STATE_OFF, "the state fits behind the ring");
+constexpr int BARRIERS = 4 + 2 * STAGES + 8 + 4 + 2 * ITEMS;
+static_assert(offsetof(SmemState, items) == BARRIERS * sizeof(uint64_t), "the barriers are one array");
 
 // A ring stage and the parity of its use; the next one.
 struct Ring {
@@ -412,26 +416,17 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     return;
   }
 
-  if (warp == LOAD_WARP && lane == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm.q_full[i]), 1);
-      mbar_init(smem_u32(&sm.q_empty[i]), 1);
-      mbar_init(smem_u32(&sm.pv_done[i]), 1);
-      mbar_init(smem_u32(&sm.o_full[i]), 1);
-    }
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&sm.ring_full[i]), 1);
-      mbar_init(smem_u32(&sm.ring_empty[i]), 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.p_full[i]), SOFTMAX_WARPS / 2);
-    }
-    for (int i = 0; i < ITEMS; ++i) {
-      mbar_init(smem_u32(&sm.item_full[i]), 1);
-      mbar_init(smem_u32(&sm.item_empty[i]), 1 + SOFTMAX_WARPS);  // the issuer and the softmax warps
+  if (warp == LOAD_WARP) {
+    for (int i = lane; i < BARRIERS; i += 32) {
+      const uint64_t* const bar = sm.q_full + i;
+      const bool p_bar = bar >= sm.p_full && bar < sm.p_full + 4;
+      const bool item_bar = bar >= sm.item_empty;  // the issuer and the softmax warps
+      mbar_init(smem_u32(bar), p_bar ? SOFTMAX_WARPS / 2 : item_bar ? 1 + SOFTMAX_WARPS : 1);
     }
     fence_mbar_init();
+    __syncwarp();
+  }
+  if (warp == LOAD_WARP && lane == 0) {
     tma_prefetch_desc(&p.q);
     tma_prefetch_desc(&p.k);
     tma_prefetch_desc(&p.v);
@@ -454,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     mine += head_units(req, p.tQ_shift) * p.n_kv_head;
   }
   long long upto = mine;
-#pragma unroll
+#pragma unroll 1  // short code: its instructions are fetched for one use
   for (int o = 1; o < 32; o <<= 1) {
     const long long up = __shfl_up_sync(FULL, upto, o);
     if (lane >= o) upto += up;
@@ -464,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   __syncthreads();
   tc_fence_after();
   long long total = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) upto += sm.warp_sum[w];
     total += sm.warp_sum[w];
@@ -837,14 +832,22 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           // behind the arithmetic (96 registers a thread, for 16 warps).
           const bool edge = __any_sync(FULL, min(limit[0], limit[1]) < k0 + BK);
           uint32_t va[16], vb[16];  // 32 keys each
-          auto mask = [&](uint32_t(&v)[16], int y) {
-            if (edge) {
+          if (edge) {
+            // Masked scores are made -inf in TMEM, 32 keys at a time in a loop: a fifth of the
+            // instructions of masking the registers, which a decode step would fetch for one tile.
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y) {
+              const int key = k0 + 32 * y + quad * 2;
+              if (!__any_sync(FULL, min(limit[0], limit[1]) < k0 + 32 * y + 32)) continue;
+              tmem_ld_quad4(scol + 32 * y, va);
+              tmem_wait_quad4(va);
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (k0 + 32 * y + (i >> 2) * 8 + quad * 2 + (i & 1) >= limit[(i >> 1) & 1])
-                  v[i] = __float_as_uint(-INFINITY);
+                if (key + (i >> 2) * 8 + (i & 1) >= limit[(i >> 1) & 1]) va[i] = __float_as_uint(-INFINITY);
+              tmem_st_quad4(scol + 32 * y, va);
             }
-          };
+            tmem_wait_st();
+          }
           auto row_max = [&](const uint32_t(&v)[16], int x) {
             float mx[2];
 #pragma unroll
@@ -860,8 +863,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             tmem_ld_quad4(scol + 64 * y, va);
             tmem_ld_quad4(scol + 64 * y + 32, vb);
             tmem_wait_quad4(va, vb);
-            mask(va, 2 * y);
-            mask(vb, 2 * y + 1);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const float a = fmaxf(row_max(va, x), row_max(vb, x));
@@ -925,8 +926,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           weights(vb, 3);
           tmem_ld_quad4(scol + 32, vb);
           tmem_wait_quad4(va, vb);
-          mask(va, 0);
-          mask(vb, 1);
           weights(va, 0);
           weights(vb, 1);
           l[0] += ls[0].x + ls[0].y;
@@ -1055,17 +1054,56 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 
 // Joins the partials of the work tile that begins in range blockIdx.y and ends in a later one:
 // out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over its parts in the order of the keys
-// (slot 2 c + 1 of the first CTA, slots 2 c of the others).  Eight blocks per work tile: of 32
-// rows each, or, where it has no more rows than that (a decode token has G, and up to 152
-// parts), of two column groups each; there the threads share the parts of an element, every
-// n-th one each, and their sums are added in a fixed order.  The first loads of O are on their
-// way before the weights are known.  Bound by latency: two dependent loads behind the launch.
+// (slot 2 c + 1 of the first CTA, slots 2 c of the others), in one pass with the running M.
+// Eight blocks per work tile: of 32 rows each, or, where it has no more rows than that (a decode
+// token has G, and up to 152 parts), of two column groups each; there `share` threads share an
+// element, every n-th part each, and their sums are joined in a fixed order.  A thread keeps to
+// one row, so it needs no one else's weights.  Bound by latency: the launch, the instructions'
+// own first fetch, two dependent loads.
 constexpr int COMBINE_THREADS = 256;
 constexpr int COMBINE_BLOCKS = 8;
+struct Joined {  // of some parts: running maximum, sum, weighted O
+  float top, sum;
+  float4 o;
+};
+__device__ __forceinline__ void join(Joined& a, float m, float l, const float4& x) {
+  const float next = fmaxf(a.top, m);
+  if (next == -INFINITY) return;  // no key yet; what a part without keys holds is never used
+  const float f = ex2(a.top - next), w = ex2(m - next);
+  a.top = next;
+  a.sum = a.sum * f + w * l;
+  if (w != 0.f) a.o = make_float4(a.o.x * f + w * x.x, a.o.y * f + w * x.y, a.o.z * f + w * x.z, a.o.w * f + w * x.w);
+}
+// K column groups of a row, U parts' loads at a time.
+template <int K, int U>
+__device__ __forceinline__ void join_parts(const PagedParams& p, int c, int nparts, int row, int c8, int first, int share,
+                                           bool in_row, Joined (&a)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) a[k] = Joined{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i0 = first; i0 < nparts; i0 += U * share) {
+    float4 x[U][K];
+    float m[U], l[U];
+#pragma unroll
+    for (int b = 0; b < U; ++b) {
+      const int i = i0 + b * share;
+      const bool in = in_row && i < nparts;
+      const uint8_t* const part = p.parts + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * PART_BYTES;
+      const float* const ml = reinterpret_cast<const float*>(part + PART_O) + row;
+      m[b] = in ? ml[0] : -INFINITY;
+      l[b] = in ? ml[256] : 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        x[b][k] = in ? reinterpret_cast<const float4*>(part)[((c8 + 4 * k) * 256 + row) * 2 + (threadIdx.x & 1)]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int b = 0; b < U; ++b)
+#pragma unroll
+      for (int k = 0; k < K; ++k) join(a[k], m[b], l[b], x[b][k]);
+  }
+}
 __global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const __grid_constant__ PagedParams p) {
-  __shared__ float s_w[CTAS][32];  // each part's weight per row
-  __shared__ float s_inv[32];
-  __shared__ float4 s_sum[COMBINE_THREADS];
+  __shared__ Joined s_part[COMBINE_THREADS];
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.y, bx = blockIdx.x;
@@ -1075,106 +1113,39 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const
   const bool wide = all > 32;
   const int row0 = wide ? bx * 32 : 0, rows = min(32, all - row0);
   if (rows <= 0) return;
-  const int nparts = s.last - c + 1;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * PART_BYTES; };
-  auto place = [&](int r) {  // row of the partial
-    const int m = row0 + r;
-    return m < half0 ? m : 128 + m - half0;
+  const int nparts = s.last - c + 1, tid = threadIdx.x;
+  // Thread number: float4 of a column group (1 bit), row (`shift` bits), column group (2 bits, and
+  // three more at distances of 4; or 1 bit), share.
+  const int shift = wide || rows > 16 ? 5 : 32 - __clz(rows - 1);  // rows <= 2^shift
+  const int r = (tid >> 1) & ((1 << shift) - 1), hi = tid >> (1 + shift);
+  const int m = row0 + r, row = m < half0 ? m : 128 + m - half0;
+  const int tok = m / p.G;  // row m is token m / G, head m % G
+  const long long out_row = (long long)(s.row0 + tok) * p.n_head + s.g * p.G + (m - tok * p.G);
+  auto store = [&](const Joined& a, int c8) {
+    const float inv = a.sum > 0.f ? 1.0f / a.sum : 0.f;
+    reinterpret_cast<uint2*>(p.out + out_row * HD)[c8 * 2 + (tid & 1)] =
+        inv > 0.f ? make_uint2(pack_bf16x2(a.o.x * inv, a.o.y * inv), pack_bf16x2(a.o.z * inv, a.o.w * inv))
+                  : make_uint2(0, 0);
+    if (p.lse && c8 == 0 && (tid & 1) == 0) p.lse[out_row] = a.sum > 0.f ? (a.top + log2f(a.sum)) * LN2 : -INFINITY;
   };
-  auto out_row = [&](int r) {  // row m is token m / G, head m % G
-    const int tok = (row0 + r) / p.G;
-    return (long long)(s.row0 + tok) * p.n_head + s.g * p.G + (row0 + r - tok * p.G);
-  };
-  // float4 x of row r, column group c8: two per group, 2^shift rows together.
-  int shift = 5;
-  if (!wide)
-    while (shift > 0 && 1 << (shift - 1) >= rows) --shift;
-  const int elems = wide ? 1024 : 4 << shift;  // of the block
-  const int share = wide ? 1 : COMBINE_THREADS / elems, first = wide ? 0 : tid / elems;
-  auto locate = [&](int e, int& r, int& c4) {
-    r = (e >> 1) & ((1 << shift) - 1);
-    c4 = 2 * ((e >> (shift + 1)) + (wide ? 0 : 2 * bx)) + (e & 1);
-  };
-  auto load = [&](int i, int r, int c4) {
-    return reinterpret_cast<const float4*>(part(i))[((c4 >> 1) * 256 + place(r)) * 2 + (c4 & 1)];
-  };
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 x[8];  // wide: parts 0 and 1 of four elements; else eight parts of one
+  if (wide) {  // its last rows may be few: the others' threads stay idle
+    Joined a[4];
+    join_parts<4, 1>(p, c, nparts, row, hi, 0, 1, r < rows, a);
+    if (r < rows)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    int r, c4;
-    locate(wide ? tid + (k >> 1) * COMBINE_THREADS : tid & (elems - 1), r, c4);
-    const int i = wide ? k & 1 : first + k * share;
-    x[k] = r < rows && i < nparts ? load(i, r, c4) : zero;
-  }
-  // One warp per row: the largest maximum, the weights, the sum.
-  for (int r = warp; r < rows; r += COMBINE_THREADS / 32) {
-    const int at = place(r);
-    float top = -INFINITY, mi = -INFINITY, li = 0.f;
-    for (int i = lane; i < nparts; i += 32) {
-      const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
-      mi = ml[at];
-      li = ml[256 + at];
-      top = fmaxf(top, mi);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-    float sum = 0.f;
-    for (int i = lane; i < nparts; i += 32) {
-      if (nparts > 32) {
-        const float* ml = reinterpret_cast<const float*>(part(i) + PART_O);
-        mi = ml[at];
-        li = ml[256 + at];
-      }
-      const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
-      s_w[i][r] = w;
-      sum += w * li;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-    if (lane == 0) {
-      s_inv[r] = sum > 0.f ? 1.0f / sum : 0.f;
-      if (p.lse && (wide || bx == 0)) p.lse[out_row(r)] = sum > 0.f ? (top + log2f(sum)) * LN2 : -INFINITY;
-    }
-  }
-  __syncthreads();
-  auto add = [](float4& o, float w, const float4& v) {  // a weight of 0 hides what the part holds
-    if (w != 0.f) o = make_float4(o.x + w * v.x, o.y + w * v.y, o.z + w * v.z, o.w + w * v.w);
-  };
-  auto store = [&](int r, int c4, const float4& o) {
-    const float inv = s_inv[r];
-    reinterpret_cast<uint2*>(p.out + out_row(r) * HD)[c4] =
-        inv > 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0, 0);
-  };
-  if (wide) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      int r, c4;
-      locate(tid + k * COMBINE_THREADS, r, c4);
-      if (r >= rows) continue;
-      float4 o = zero;
-      add(o, s_w[0][r], x[2 * k]);
-      add(o, s_w[1][r], x[2 * k + 1]);
-      for (int i = 2; i < nparts; ++i) add(o, s_w[i][r], load(i, r, c4));
-      store(r, c4, o);
-    }
+      for (int k = 0; k < 4; ++k) store(a[k], hi + 4 * k);
   } else {
-    int r, c4;
-    locate(tid & (elems - 1), r, c4);
-    float4 o = zero;
-    if (r < rows) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (first + k * share < nparts) add(o, s_w[first + k * share][r], x[k]);
-#pragma unroll 4
-      for (int i = first + 8 * share; i < nparts; i += share) add(o, s_w[i][r], load(i, r, c4));
-    }
-    s_sum[tid] = o;
+    Joined a[1];
+    const int first = hi >> 1, share = 64 >> shift;
+    join_parts<1, 4>(p, c, nparts, row, 2 * bx + (hi & 1), first, share, r < rows, a);
+    s_part[tid] = a[0];
     __syncthreads();
     if (first == 0 && r < rows) {
-      for (int i = 1; i < share; ++i) add(o, 1.0f, s_sum[i * elems + tid]);
-      store(r, c4, o);
+      for (int i = 1; i < share; ++i) {
+        const Joined& y = s_part[tid + i * (4 << shift)];
+        join(a[0], y.top, y.sum, y.o);
+      }
+      store(a[0], 2 * bx + (hi & 1));
     }
   }
 }
