@@ -151,14 +151,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_torch_c = None
+
+
 def _stream(stream):
     """The stream's handle; by default PyTorch's current stream of the current device.  Read
     from PyTorch's own per-device word (0.3 us): building a Stream object for it takes 3 us, as
     long as a launch."""
+    global _torch_c
     if stream is not None:
         return stream.cuda_stream
-    from torch import _C
-    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    if _torch_c is None:
+        from torch import _C
+        _torch_c = _C
+    return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
 
 
 def _check(name: str, code: int):

@@ -189,7 +189,6 @@ __device__ __forceinline__ uint64_t kv_desc(uint32_t addr) {
 }
 
 struct SmemState {
-  // Barriers, one array after the other.
   uint64_t q_full[2], q_empty[2];
   uint64_t ring_full[STAGES], ring_empty[STAGES];
   uint64_t s_full[4];    // pair: half 0, 1; single: even, odd key tile
@@ -205,8 +204,6 @@ struct SmemState {
   uint32_t tmem;
 };
 static_assert(sizeof(SmemState) <= SMEM_BYTES - STATE_OFF, "the state fits behind the ring");
-constexpr int BARRIERS = 4 + 2 * STAGES + 8 + 4 + 2 * ITEMS;
-static_assert(offsetof(SmemState, items) == BARRIERS * sizeof(uint64_t), "the barriers are one array");
 
 // A ring stage and the parity of its use; the next one.
 struct Ring {
@@ -416,17 +413,26 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     return;
   }
 
-  if (warp == LOAD_WARP) {
-    for (int i = lane; i < BARRIERS; i += 32) {
-      const uint64_t* const bar = sm.q_full + i;
-      const bool p_bar = bar >= sm.p_full && bar < sm.p_full + 4;
-      const bool item_bar = bar >= sm.item_empty;  // the issuer and the softmax warps
-      mbar_init(smem_u32(bar), p_bar ? SOFTMAX_WARPS / 2 : item_bar ? 1 + SOFTMAX_WARPS : 1);
+  if (warp == LOAD_WARP && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_full[i]), 1);
+      mbar_init(smem_u32(&sm.q_empty[i]), 1);
+      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+      mbar_init(smem_u32(&sm.o_full[i]), 1);
+    }
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&sm.ring_full[i]), 1);
+      mbar_init(smem_u32(&sm.ring_empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_full[i]), SOFTMAX_WARPS / 2);
+    }
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(smem_u32(&sm.item_full[i]), 1);
+      mbar_init(smem_u32(&sm.item_empty[i]), 1 + SOFTMAX_WARPS);  // the issuer and the softmax warps
     }
     fence_mbar_init();
-    __syncwarp();
-  }
-  if (warp == LOAD_WARP && lane == 0) {
     tma_prefetch_desc(&p.q);
     tma_prefetch_desc(&p.k);
     tma_prefetch_desc(&p.v);
@@ -832,22 +838,14 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           // behind the arithmetic (96 registers a thread, for 16 warps).
           const bool edge = __any_sync(FULL, min(limit[0], limit[1]) < k0 + BK);
           uint32_t va[16], vb[16];  // 32 keys each
-          if (edge) {
-            // Masked scores are made -inf in TMEM, 32 keys at a time in a loop: a fifth of the
-            // instructions of masking the registers, which a decode step would fetch for one tile.
-#pragma unroll 1
-            for (int y = 0; y < 4; ++y) {
-              const int key = k0 + 32 * y + quad * 2;
-              if (!__any_sync(FULL, min(limit[0], limit[1]) < k0 + 32 * y + 32)) continue;
-              tmem_ld_quad4(scol + 32 * y, va);
-              tmem_wait_quad4(va);
+          auto mask = [&](uint32_t(&v)[16], int y) {
+            if (edge) {
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (key + (i >> 2) * 8 + (i & 1) >= limit[(i >> 1) & 1]) va[i] = __float_as_uint(-INFINITY);
-              tmem_st_quad4(scol + 32 * y, va);
+                if (k0 + 32 * y + (i >> 2) * 8 + quad * 2 + (i & 1) >= limit[(i >> 1) & 1])
+                  v[i] = __float_as_uint(-INFINITY);
             }
-            tmem_wait_st();
-          }
+          };
           auto row_max = [&](const uint32_t(&v)[16], int x) {
             float mx[2];
 #pragma unroll
@@ -863,6 +861,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             tmem_ld_quad4(scol + 64 * y, va);
             tmem_ld_quad4(scol + 64 * y + 32, vb);
             tmem_wait_quad4(va, vb);
+            mask(va, 2 * y);
+            mask(vb, 2 * y + 1);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const float a = fmaxf(row_max(va, x), row_max(vb, x));
@@ -926,6 +926,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           weights(vb, 3);
           tmem_ld_quad4(scol + 32, vb);
           tmem_wait_quad4(va, vb);
+          mask(va, 0);
+          mask(vb, 1);
           weights(va, 0);
           weights(vb, 1);
           l[0] += ls[0].x + ls[0].y;

@@ -242,7 +242,7 @@ struct AppendParams {
 // Half a warp per head, 16 bytes per lane; up to sixteen heads' loads are on their way before
 // the first reduction.  Bound by the memory system: 8192 rows of 8 + 2 + 2 heads move 50 MB.
 constexpr int APPEND_PAIRS = 8;
-__global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256, 4) paged_append_kernel(const AppendParams p) {
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
