@@ -18,8 +18,12 @@ import pytest
 import torch
 
 import aux_loss_free_gb300 as M
-from gpu_util import bf16_to_np
+from gpu_util import assert_close_bf16, bf16_to_np, bf64
+from oracle import attention_oracle as A
 from oracle import paged_oracle as P
+from synth import ATTN_CONFIGS, make_attention
+from aux_loss_free_gb300.layer import to_device_bf16
+from aux_loss_free_gb300.paged import PagedAttention, PagedStep
 
 pytestmark = pytest.mark.gpu
 
@@ -515,3 +519,48 @@ def test_plan_append_attention_in_a_captured_graph():
         ctx.copy_(nxt)
         state.copy_(state_out)
         assert (bf16_to_np(out)[at:] == 0).all()
+
+
+@pytest.mark.parametrize("residual", [True, False])
+def test_block_in_steps_matches_the_dense_oracle(residual):
+    """Three sequences through the whole block in uneven steps, one of them in a row of the
+    block table that another request has left, against the dense oracle on each sequence (the
+    block tests' tolerance); padding rows come out as x (or zero)."""
+    a = ATTN_CONFIGS["attn_tiny"].replace(batch=1, seq=150, n_head=8, n_kv_head=2, d=512)
+    H = make_attention(a, "attn_tiny")
+    w_qkv = to_device_bf16(np.concatenate([H["w_q"], H["w_k"], H["w_v"]], axis=0), DEV)
+    step = PagedStep(requests=3, pages=20, page_size=16, max_pages=10, max_tokens=160)
+    block = PagedAttention(step, a.d, 8, 2, w_qkv, to_device_bf16(H["w_o"], DEV), a.eps)
+    rng = np.random.default_rng(21)
+    script = [([40, 0, 7], 3), ([1, 90, 1], 0), ([50, 1, 0], 5), ([-1, 1, 30], 0), ([0, 3, 1], 1), ([60, 1, -1], 0),
+              ([1, 1, 0], 6)]
+    seqs, rows_of, got = {}, {0: "a", 1: "b", 2: "c"}, {}
+    for lens, pad in script:
+        T = sum(max(n, 0) for n in lens) + pad
+        x = _rows(rng, max(T, 1), a.d)
+        out = torch.full_like(x, 9.0)
+        block.forward(x, step.plan(_i32(lens), x.shape[0]) and out, residual=residual)
+        torch.cuda.synchronize()
+        at = 0
+        for r, n in enumerate(lens):
+            if n < 0:
+                rows_of[r] += "'"
+            elif n:
+                seqs.setdefault(rows_of[r], []).append(bf16_to_np(x)[at:at + n])
+                got.setdefault(rows_of[r], []).append(bf16_to_np(out)[at:at + n])
+                at += n
+        assert np.array_equal(bf16_to_np(out)[at:], bf16_to_np(x)[at:] if residual else np.zeros((x.shape[0] - at, a.d)))
+        assert step.info.tolist()[3] == 0
+    w = [bf64(H[n]) for n in ("w_q", "w_k", "w_v", "w_o")]
+    assert sorted(seqs) == ["a", "a'", "b", "c"]
+    for name, parts in seqs.items():
+        xs = np.concatenate(parts)
+        ref = A.gqa_attention(xs, *w, 1, len(xs), 8, 2, 128, a.eps, residual=residual, round_stored=True)
+        assert_close_bf16(np.concatenate(got[name]), ref["out"], f"sequence {name}")
+    assert step.free_pages.item() == 20 - -(-61 // 16) - -(-98 // 16)
+
+
+def test_step_refuses_more_rows_than_it_was_made_for():
+    step = PagedStep(requests=2, pages=4, page_size=16, max_pages=2, max_tokens=8)
+    with pytest.raises(ValueError):
+        step.plan(_i32([9, 0]), 9)
