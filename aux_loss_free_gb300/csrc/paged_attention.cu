@@ -971,13 +971,13 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       uint16_t* dst[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        inv[x] = l[x] > 0.f ? 1.0f / l[x] : 0.f;
+        inv[x] = l[x] != 0.f ? 1.0f / l[x] : 0.f;  // 0: no keys; a NaN among the scores stays one
         const int mr = lane0 + lane / 4 + 8 * x, tok_in = mr / p.G;
         const long long row = (long long)(it.row0 + (pair ? wg * p.tq : 0) + tok_in) * p.n_head + it.g * p.G +
                               (mr - tok_in * p.G);
         dst[x] = p.out + row * HD + quad * 8;
         if (it.part < 0 && (valid >> x & 1) && p.lse && quad == 0)
-          p.lse[row] = l[x] > 0.f ? (m[x] + log2f(l[x])) * LN2 : -INFINITY;
+          p.lse[row] = l[x] != 0.f ? (m[x] + log2f(l[x])) * LN2 : -INFINITY;
       }
       if (!adds && !half_wait(&sm.o_full[wg], outs, wg, p.status)) break;
       ++outs;
@@ -990,9 +990,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                w[i] = inv[x] > 0.f ? pack_bf16x2(__uint_as_float(o[4 * i + 2 * x]) * inv[x],
+                w[i] = inv[x] != 0.f ? pack_bf16x2(__uint_as_float(o[4 * i + 2 * x]) * inv[x],
                                                   __uint_as_float(o[4 * i + 2 * x + 1]) * inv[x])
-                                    : 0u;
+                                     : 0u;
               // Four lanes hold one pair each of each of four groups; lane i of the quad is to have
               // group i whole: a 4 x 4 transposition, so that a lane stores 16 bytes and a quad 64
               // of its row.
@@ -1078,7 +1078,10 @@ struct Joined {  // of some parts: running maximum, sum, weighted O
 };
 __device__ __forceinline__ void join(Joined& a, float m, float l, const float4& x) {
   const float next = fmaxf(a.top, m);
-  if (next == -INFINITY) return;  // no key yet; what a part without keys holds is never used
+  if (next == -INFINITY) {  // no key yet: what a part without keys holds is never used, its sum
+    a.sum += l;             // is 0, or NaN where every score was
+    return;
+  }
   const float f = ex2(a.top - next), w = ex2(m - next);
   a.top = next;
   a.sum = a.sum * f + w * l;
@@ -1132,11 +1135,11 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const
   const int tok = m / p.G;  // row m is token m / G, head m % G
   const long long out_row = (long long)(s.row0 + tok) * p.n_head + s.g * p.G + (m - tok * p.G);
   auto store = [&](const Joined& a, int c8) {
-    const float inv = a.sum > 0.f ? 1.0f / a.sum : 0.f;
+    const float inv = a.sum != 0.f ? 1.0f / a.sum : 0.f;
     reinterpret_cast<uint2*>(p.out + out_row * HD)[c8 * 2 + (tid & 1)] =
-        inv > 0.f ? make_uint2(pack_bf16x2(a.o.x * inv, a.o.y * inv), pack_bf16x2(a.o.z * inv, a.o.w * inv))
-                  : make_uint2(0, 0);
-    if (p.lse && c8 == 0 && (tid & 1) == 0) p.lse[out_row] = a.sum > 0.f ? (a.top + log2f(a.sum)) * LN2 : -INFINITY;
+        inv != 0.f ? make_uint2(pack_bf16x2(a.o.x * inv, a.o.y * inv), pack_bf16x2(a.o.z * inv, a.o.w * inv))
+                   : make_uint2(0, 0);
+    if (p.lse && c8 == 0 && (tid & 1) == 0) p.lse[out_row] = a.sum != 0.f ? (a.top + log2f(a.sum)) * LN2 : -INFINITY;
   };
   if (wide) {  // its last rows may be few: the others' threads stay idle
     Joined a[4];

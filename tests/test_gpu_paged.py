@@ -334,6 +334,36 @@ def test_attention_never_uses_what_lies_past_the_keys(stale):
     _check_attention(_attn_inputs(rng, [130, 9, 0], [1, 40, 1], 8, 2, 64, 1, stale=stale))
 
 
+# (ctx, new, positions of request 0 whose keys of key/value head 0 are NaN)
+NAN_KEYS = {
+    "decode": ([300], [1], (17, 18)),
+    "decode-every-key": ([300], [1], (0, 301)),
+    "decode-in-parts": ([9000, 40], [1, 1], (5000, 5001)),
+    "decode-whole-parts": ([9000, 40], [1, 1], (0, 4000)),
+    "few-rows-in-parts": ([9000, 9100], [3, 5], (9001, 9002)),
+    "chunk": ([100], [200], (230, 231)),
+    "chunk-in-many-parts": ([20000], [64], (0, 15000)),
+    "chunks-in-three-parts": ([6000, 5000], [700, 27], (6300, 6301)),
+}
+
+
+@pytest.mark.parametrize("name", NAN_KEYS)
+def test_attention_rows_that_see_a_nan_are_nan_and_no_others(name):
+    ctx, new, (first, last) = NAN_KEYS[name]
+    a = _attn_inputs(np.random.default_rng(21), ctx, new, 8, 2, 16, pad=1)
+    ref_out, ref_lse = _attend(a)
+    pos = np.arange(first, last)
+    b = dict(a, k=a["k"].clone())
+    b["k"][torch.tensor(a["table"][0][pos // 16], device=DEV), 0, torch.tensor(pos % 16, device=DEV)] = float("nan")
+    out, lse = _attend(b)
+    sees = torch.zeros(out.shape[0], 8, dtype=torch.bool, device=DEV)
+    sees[:new[0], :4] = (torch.arange(ctx[0], ctx[0] + new[0], device=DEV) >= first)[:, None]
+    assert torch.isnan(lse[sees]).all() and torch.equal(lse[~sees], ref_lse[~sees])
+    out, ref_out = out.reshape(-1, 8, 128), ref_out.reshape(-1, 8, 128)
+    assert torch.isnan(out[sees]).all()
+    assert torch.equal(out[~sees].view(torch.int16), ref_out[~sees].view(torch.int16))
+
+
 def test_attention_of_denied_requests_and_padding_is_zero():
     a = _attn_inputs(np.random.default_rng(4), [50, 300, 20, 10], [1, 70, 2, 1], 8, 2, 16, pad=300)
     a["kv"][[1, 3]] = 0  # denied: no keys, whatever the rows
