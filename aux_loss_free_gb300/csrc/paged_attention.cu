@@ -32,7 +32,10 @@
 //     value tiles, into a ring of five 32 KB stages;
 //   - warp 17 (one thread) issues tcgen05.mma: S = Q K^T into a score buffer, O += P V with P
 //     (bf16) read from the score buffer's own columns.  The pipe runs in order, so a score
-//     product that overwrites a buffer needs no wait for the product that read P from it;
+//     product that overwrites a buffer needs no wait for the product that read P from it.  A
+//     pair's P comes in three parts (keys 64-127, 0-31, 32-63): the value product of a part runs
+//     while the next is computed, and only the last one's lies between the softmax and the next
+//     scores (one part: 138 us, two: 129, three: 127 for 2 x 2011 tokens over long contexts);
 //   - warps 0-7 and 8-15, a warp per 16 rows: the online softmax in the log2 domain.  TMEM is
 //     read in the 16 x 256-bit shape, four lanes per row with 32 scores each, so that two
 //     warps per SM sub-partition share a half tile and the row maximum is two shuffles; O is
@@ -44,12 +47,14 @@
 // Every barrier wait is bounded; on a timeout the status word is set and the CTA exits.
 //
 // Bounds and measurements (8 query heads on 2 key/value heads; time of a call among others).
-// One token for each of 64 requests with 1000 to 16000 keys: 549 MB of keys and values, 93.6 us,
+// One token for each of 64 requests with 1000 to 16000 keys: 549 MB of keys and values, 92.5 us,
 // 5.9 TB/s; between its first copy and its last output a CTA streams at 6.3 TB/s, the rest is the
 // start (6 us: two dependent loads, the first copies and each instruction's first fetch) and the
-// joins (5 us).  2 x 2011 tokens over 1000 to 14000 keys: 176 GFLOP, 140 us, 1.26 PFLOP/s: the
-// tensor pipe waits for the softmax, a chain of 1.5k cycles per half tile against the 1024 of the
-// other half's products.  Both limits are latency; neither memory nor the pipe is saturated.
+// joins (5 us).  2 x 2011 tokens over 1000 to 14000 keys: 176 GFLOP, 127 us, 1.39 PFLOP/s: a half
+// tile's chain (3.1k cycles: 0.75k maximum, 1.0k weights, 1.3k from the last part of P over its
+// value product and the next scores back to the warps) is longer than both halves' products (2k),
+// and tensor memory has no columns for a third half.  Both limits are latency; neither memory nor
+// the pipe is saturated.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -78,6 +83,7 @@ constexpr int THREADS = 576;
 constexpr int WARPS = THREADS / 32;
 constexpr int ITEMS = 4;                      // depth of the item ring
 constexpr int CTAS = 152;                     // one per SM
+constexpr int P_PARTS = 3;                     // hardware barriers 3 .. 8: P's three parts, each of the two halves
 constexpr uint32_t O_COL = 256;               // score buffers at 0 and 128, outputs at 256 and 384
 constexpr uint32_t TMEM_COLS = 512;
 constexpr unsigned FULL = 0xFFFFFFFFu;
@@ -201,7 +207,7 @@ struct SmemState {
   uint64_t q_full[2], q_empty[2];
   uint64_t ring_full[STAGES], ring_empty[STAGES];
   uint64_t s_full[4];    // pair: half 0, 1; single: even, odd key tile
-  uint64_t p_full[4];
+  uint64_t p_full[2];    // single: even, odd key tile
   uint64_t pv_done[2];   // single: even, odd key tile
   uint64_t o_full[2];
   uint64_t item_full[ITEMS], item_empty[ITEMS];
@@ -209,6 +215,7 @@ struct SmemState {
   long long warp_sum[WARPS];
   long long start_off;   // units of the starting request before the range
   int start_req;
+  int dead;              // the issuer has given up
   Request start;
   uint32_t tmem;
 };
@@ -280,12 +287,32 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // The same for the eight warps of a query half (hardware barrier 1 + wg): one lane of the first
-// warp polls, the others sleep at the barrier, which hands them the outcome.  Sixteen polling
-// warps slow the loading and the issuing warp down several times (measured: 2.4 us instead of
-// 0.4 us for the walk's start).
-__device__ __forceinline__ bool half_wait(const uint64_t* bar, uint32_t parity, int wg, int* status) {
+// warp polls, the others sleep at the barrier, which hands them the outcome; sixteen polling warps
+// slow the loading and the issuing warp down (a call's start: 2.4 us to the first score product
+// instead of 1.7).  With `dead` the wait gives up, past its limit, only once the issuer has: the
+// issuer's waits for the parts of P have no limit of their own, and end because a half that has an
+// item hands over every part of it.
+// TRIES tests in a row before the clock is read; for the scores 32 measured best (a test per loop
+// 137 us, 4 or 8 133, 32 or 64 127 for the 2 x 2011 tokens), where the wait is once per item the
+// short code does (its instructions are fetched anew by every launch).
+template <int TRIES>
+__device__ __forceinline__ uint32_t poll(uint32_t bar, uint32_t parity, int* status, const int* dead) {
+  if (mbar_try_wait(bar, parity)) return 1;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < TRIES; ++i)
+      if (mbar_try_wait(bar, parity)) return 1;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(status, kDevTimeout);
+      if (!dead || *(const volatile int*)dead) return 0;
+    }
+  }
+}
+template <int TRIES = 4>
+__device__ __forceinline__ bool half_wait(const uint64_t* bar, uint32_t parity, int wg, int* status, const int* dead) {
   uint32_t ok = 1;
-  if (threadIdx.x % 256 == 0) ok = mbar_wait(smem_u32(bar), parity & 1u, status) ? 1 : 0;
+  if (threadIdx.x % 256 == 0) ok = poll<TRIES>(smem_u32(bar), parity & 1u, status, dead);
   __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -296,6 +323,18 @@ __device__ __forceinline__ bool half_wait(const uint64_t* bar, uint32_t parity, 
       : "r"(ok), "r"(1 + wg)
       : "memory");
   return ok != 0;
+}
+
+// Hardware barriers between the eight warps of a query half, which arrive, and the issuing warp,
+// which waits: no test of a barrier in shared memory, which takes some 250 cycles while the tensor
+// pipe reads operands there.  In the form that counts threads: no warp has to be converged.
+__device__ __forceinline__ void part_arrive(int id) {
+  __syncwarp();
+  asm volatile("barrier.cta.arrive %0, 288;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void part_wait(int id) {
+  __syncwarp();
+  asm volatile("barrier.cta.sync %0, 288;" ::"r"(id) : "memory");
 }
 
 // TMEM in the 16 x 256-bit shape: sixteen rows, `n` groups of eight fp32 columns; a lane holds
@@ -399,6 +438,7 @@ __device__ __forceinline__ void add_part(const uint8_t* part, unsigned long long
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       v[k] = w[k & 1] != 0.f ? __ldcg(po + (y * 4 + (k >> 1)) * 1024 + (k & 1) * 32) : make_float2(0.f, 0.f);
+    __syncwarp();
     tmem_wait_quad4(o);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -434,12 +474,13 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.p_full[i]), SOFTMAX_WARPS / 2);
+      if (i < 2) mbar_init(smem_u32(&sm.p_full[i]), SOFTMAX_WARPS / 2);
     }
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(smem_u32(&sm.item_full[i]), 1);
       mbar_init(smem_u32(&sm.item_empty[i]), 1 + SOFTMAX_WARPS);  // the issuer and the softmax warps
     }
+    sm.dead = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.q);
     tma_prefetch_desc(&p.k);
@@ -656,7 +697,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     constexpr uint32_t id_s = idesc_bf16_f32(128, BK, 0, 0);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, 0, 1);
     const bool issues = elect_one();
-    uint32_t q_uses[2] = {0, 0}, pairs = 0, even = 0, odd = 0;
+    uint32_t q_uses[2] = {0, 0}, even = 0, odd = 0;
     Ring key{0, 0};  // of the next key tile; its value tile is the stage behind
     auto score = [&](int half, int buf, uint32_t st) {  // S[buf] = Q[half] K^T
       const uint64_t qd = sw128_kmajor_desc(base + half * TILE_BYTES);
@@ -668,13 +709,14 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
                       kd + (kk >> 2) * (1024 >> 4) + 2 * (kk & 3), id_s, kk != 0);
       }
     };
-    auto value = [&](int out, int buf, uint32_t st, bool first) {  // O[out] (+)= P[buf] V
+    // O[out] (+)= P[buf] V for `n` steps of 16 keys from step k0 on; `first` of the item's.
+    auto value = [&](int out, int buf, uint32_t st, int k0, int n, bool first) {
       const uint64_t vd = kv_desc(base + RING_OFF + st * TILE_BYTES);
       if (issues) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
+        for (int kk = k0; kk < k0 + n; ++kk)
           tc_mma_bf16_a_tmem(tmem + O_COL + out * HD, tmem + buf * BK + (kk >> 2) * 64 + (kk & 3) * 8,
-                             vd + kk * 256u, id_pv, !first || kk != 0);
+                             vd + kk * 256u, id_pv, !first || kk != k0);
       }
     };
     auto commit = [&](const uint64_t* bar) {
@@ -682,7 +724,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     };
     for (uint32_t items = 0;; ++items) {
       const int slot = items % ITEMS;
-      if (!warp_wait(&sm.item_full[slot], items / ITEMS, p.status)) break;
+      if (!warp_wait(&sm.item_full[slot], items / ITEMS, p.status)) {
+        sm.dead = 1;
+        break;
+      }
       const int nt = __shfl_sync(FULL, sm.items[slot].nt, 0), half = __shfl_sync(FULL, sm.items[slot].half, 0);
       if (issues) mbar_arrive(smem_u32(&sm.item_empty[slot]));
       if (nt == 0) break;
@@ -692,7 +737,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       q_uses[0] += pair || half == 0;
       q_uses[1] += pair || half == 1;
       auto full = [&](const Ring& r) { return smem_u32(&sm.ring_full[r.stage]); };
-      if (!warp_wait_all(full(key), key.phase, q0, q0_phase, q1, q1_phase, p.status)) break;
+      if (!warp_wait_all(full(key), key.phase, q0, q0_phase, q1, q1_phase, p.status)) {
+        sm.dead = 1;
+        break;
+      }
       tc_fence_after();
       bool ok = true;
       if (pair) {
@@ -706,13 +754,19 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           const Ring val = key.next(), next = val.next(), last = more ? next : val;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            // P, and in front of the first half the value tile and the next key tile.
-            const uint32_t pf = smem_u32(&sm.p_full[h]), pp = (pairs + t) & 1u;
-            ok = ok && (h == 0 ? warp_wait_all(pf, pp, full(val), val.phase, full(last), last.phase, p.status)
-                               : warp_wait_all(pf, pp, pf, pp, pf, pp, p.status));
-            if (!ok) break;
+            // In front of the first half the value tile and the next key tile; then P in three parts.
+            if (h == 0 && !(ok = warp_wait_all(full(val), val.phase, full(last), last.phase, full(last), last.phase,
+                                               p.status)))
+              break;
+            part_wait(P_PARTS + h);
             tc_fence_after();
-            value(h, h, val.stage, t == 0);
+            value(h, h, val.stage, 4, 4, t == 0);
+            part_wait(P_PARTS + 2 + h);
+            tc_fence_after();
+            value(h, h, val.stage, 0, 2, false);
+            part_wait(P_PARTS + 4 + h);
+            tc_fence_after();
+            value(h, h, val.stage, 2, 2, false);
             if (more) {
               score(h, h, next.stage);
               commit(&sm.s_full[h]);  // covers the value product before it
@@ -726,7 +780,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           if (more) commit(&sm.ring_empty[next.stage]);
           key = next;
         }
-        pairs += nt;
       } else {
         score(half, 0, key.stage);
         commit(&sm.s_full[2]);
@@ -737,7 +790,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           // first: a late key tile does not keep the value tile's stage.
           const int b = t & 1;
           const Ring val = key.next(), next = val.next();
-          const uint32_t pf = smem_u32(&sm.p_full[2 + b]), pp = ((b ? odd : even) + (t >> 1)) & 1u;
+          const uint32_t pf = smem_u32(&sm.p_full[b]), pp = ((b ? odd : even) + (t >> 1)) & 1u;
           bool scored = t + 1 == nt, valued = false;
           unsigned long long t0 = 0;
           for (uint32_t polls = 1; !(scored && valued); ++polls) {
@@ -752,7 +805,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             }
             if (!valued && __all_sync(FULL, mbar_test_all(pf, pp, full(val), val.phase, pf, pp))) {
               tc_fence_after();
-              value(0, b, val.stage, t == 0);
+              value(0, b, val.stage, 4, 4, t == 0);
+              value(0, b, val.stage, 0, 4, false);
               if (t + 1 == nt) commit(&sm.o_full[0]);
               commit(&sm.pv_done[b]);
               commit(&sm.ring_empty[val.stage]);
@@ -774,7 +828,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         even += (nt + 1) >> 1;
         odd += nt >> 1;
       }
-      if (!ok) break;
+      if (!ok) {
+        sm.dead = 1;
+        break;
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax warps
@@ -787,7 +844,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     bool ok = true;
     for (uint32_t items = 0; ok; ++items) {
       const int slot = items % ITEMS;
-      if (!half_wait(&sm.item_full[slot], items / ITEMS, wg, p.status)) break;
+      if (!half_wait(&sm.item_full[slot], items / ITEMS, wg, p.status, &sm.dead)) break;
       const Item& it = sm.items[slot];  // this warp's until it arrives at item_empty
       const int nt = it.nt;
       const bool pair = it.half == 2;
@@ -818,7 +875,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         const int sb = pair ? wg : 2 + b;            // barrier set
         const uint32_t scol = tl + (pair ? wg : b) * BK;
         const uint32_t ph = pair ? pairs + t : (b ? odd : even) + (t >> 1);
-        if (!half_wait(&sm.s_full[sb], ph, wg, p.status)) {
+        if (!half_wait<32>(&sm.s_full[sb], ph, wg, p.status, &sm.dead)) {
           ok = false;
           break;
         }
@@ -827,10 +884,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (k0 + BK > kvlim) {
           // Values that no row of the tile may see: rows kvlim - k0 .. 127 of the stage.
           const uint32_t vl = 2 * (tiles + t) + 1;
-          if (!half_wait(&sm.ring_full[vl % STAGES], vl / STAGES, wg, p.status)) {
-            ok = false;
-            break;
-          }
+          half_wait(&sm.ring_full[vl % STAGES], vl / STAGES, wg, p.status, nullptr);
           const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
           if (zrow >= kvlim - k0) {
             uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + (zrow >> 3) * 2048 +
@@ -839,6 +893,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             for (int x = 0; x < 8; ++x) z[x] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
           }
+          __syncwarp();
         }
         if (active) {
           // The maximum needs all 128 keys, in two loads of 64; the second one's stay in
@@ -932,19 +987,37 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           weights(va, 2);
           tmem_ld_quad4(scol, va);
           weights(vb, 3);
+          if (pair) {
+            tmem_wait_st();
+            tc_fence_before();
+            part_arrive(P_PARTS + wg);
+          }
           tmem_ld_quad4(scol + 32, vb);
           tmem_wait_quad4(va, vb);
           mask(va, 0);
           mask(vb, 1);
           weights(va, 0);
+          if (pair) {
+            tmem_wait_st();
+            tc_fence_before();
+            part_arrive(P_PARTS + 2 + wg);
+          }
           weights(vb, 1);
           l[0] += ls[0].x + ls[0].y;
           l[1] += ls[1].x + ls[1].y;
           tmem_wait_st();  // P is in TMEM before the MMA may read it
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[sb]));
+        if (pair) {
+          if (!active) {
+            part_arrive(P_PARTS + wg);
+            part_arrive(P_PARTS + 2 + wg);
+          }
+          part_arrive(P_PARTS + 4 + wg);
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[b]));
+        }
       }
       if (!ok) break;
       tiles += nt;
@@ -959,7 +1032,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       l[1] = quad_sum(l[1]);
       const bool adds = it.added && it.part < 0;
       if (__builtin_expect(adds, 0)) {
-        if (!half_wait(&sm.o_full[wg], outs, wg, p.status)) break;
+        if (!half_wait(&sm.o_full[wg], outs, wg, p.status, &sm.dead)) break;
         tc_fence_after();
         if (active)
           for (int i = 1; i <= it.added; ++i)
@@ -979,7 +1052,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (it.part < 0 && (valid >> x & 1) && p.lse && quad == 0)
           p.lse[row] = l[x] != 0.f ? (m[x] + log2f(l[x])) * LN2 : -INFINITY;
       }
-      if (!adds && !half_wait(&sm.o_full[wg], outs, wg, p.status)) break;
+      if (!adds && !half_wait(&sm.o_full[wg], outs, wg, p.status, &sm.dead)) break;
       ++outs;
       tc_fence_after();
       if (active) {
@@ -1008,6 +1081,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               const uint4 line = quad & 2 ? make_uint4(a2, a3, a0, a1) : make_uint4(a0, a1, a2, a3);
               if (valid >> x & 1) *reinterpret_cast<uint4*>(dst[x] + y * 32) = line;
             }
+            __syncwarp();
           };
           uint32_t oa[16], ob[16];  // the next columns load while these are stored
           tmem_ld_quad4(ocol, oa);
@@ -1034,6 +1108,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               if (valid >> (i & 1) & 1)
                 po[(y * 4 + (i >> 1)) * 1024 + (i & 1) * 32] =
                     make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            __syncwarp();
           }
           float* const ml = reinterpret_cast<float*>(part + PART_O) + prow;
 #pragma unroll
