@@ -594,3 +594,65 @@ def test_step_refuses_more_rows_than_it_was_made_for():
     step = PagedStep(requests=2, pages=4, page_size=16, max_pages=2, max_tokens=8)
     with pytest.raises(ValueError):
         step.plan(_i32([9, 0]), 9)
+
+
+def _dense(xs, w, a, residual=True):
+    return A.gqa_attention(xs, *w, 1, len(xs), a.n_head, a.n_kv_head, 128, a.eps, residual=residual,
+                           round_stored=True)["out"]
+
+
+def test_a_captured_step_goes_on_where_the_last_one_ended():
+    """PagedStep.plan and PagedAttention.forward captured once and replayed with other new_len,
+    an eager step between two replays, against the dense oracle on each sequence.  Capturing
+    itself moves nothing."""
+    a = ATTN_CONFIGS["attn_tiny"].replace(batch=1, seq=150, n_head=8, n_kv_head=2, d=512)
+    H = make_attention(a, "attn_tiny")
+    w_qkv = to_device_bf16(np.concatenate([H["w_q"], H["w_k"], H["w_v"]], axis=0), DEV)
+    T, R = 48, 3
+    step = PagedStep(requests=R, pages=24, page_size=16, max_pages=10, max_tokens=T)
+    block = PagedAttention(step, a.d, 8, 2, w_qkv, to_device_bf16(H["w_o"], DEV), a.eps)
+    x = torch.zeros(T, a.d, dtype=torch.bfloat16, device=DEV)
+    out, new = torch.empty_like(x), _i32([0] * R)
+    rng = np.random.default_rng(31)
+
+    def call():
+        block.forward(x, step.plan(new, T) and out)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()  # warm: a step without tokens
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    assert step.ctx_len.tolist() == [0] * R and step.free_pages.item() == 24
+    seqs, got, rows_of = {}, {}, {0: "a", 1: "b", 2: "c"}
+    script = [([20, 17, 5], "replay"), ([1, 30, 16], "replay"), ([1, 1, 1], "replay"), ([16, 1, 1], "eager"),
+              ([1, -1, 40], "replay"), ([1, 19, 1], "replay"), ([2, 1, 1], "eager"), ([1, 1, 1], "replay")]
+    ctx = [0] * R
+    for lens, how in script:
+        rows = _rows(rng, T, a.d)
+        x.copy_(rows)
+        new.copy_(_i32(lens))
+        out.fill_(9.0)
+        if how == "replay":
+            graph.replay()
+        else:
+            call()
+        torch.cuda.synchronize()
+        ctx = [0 if n < 0 else c + n for c, n in zip(ctx, lens)]
+        assert step.ctx_len.tolist() == ctx
+        assert step.free_pages.item() == 24 - sum(-(-c // 16) for c in ctx)
+        at = 0
+        for r, n in enumerate(lens):
+            if n < 0:
+                rows_of[r] += "'"
+            elif n:
+                seqs.setdefault(rows_of[r], []).append(bf16_to_np(rows)[at:at + n])
+                got.setdefault(rows_of[r], []).append(bf16_to_np(out)[at:at + n])
+                at += n
+    w = [bf64(H[n]) for n in ("w_q", "w_k", "w_v", "w_o")]
+    assert sorted(seqs) == ["a", "b", "b'", "c"]
+    for name, parts in seqs.items():
+        assert_close_bf16(np.concatenate(got[name]), _dense(np.concatenate(parts), w, a), f"sequence {name}")
