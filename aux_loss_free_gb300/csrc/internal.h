@@ -308,8 +308,10 @@ cudaError_t launch_paged_plan(const moe_paged_shape_t& s, const int32_t* ctx_len
                               int32_t* block_table, int32_t* pool, const int32_t* pool_in, int32_t* pool_out,
                               int32_t* row_start, int32_t* slot_map, int32_t* kv_len, int32_t* next_ctx, int32_t* info,
                               cudaStream_t st);
-cudaError_t launch_paged_append(const moe_paged_shape_t& s, const uint16_t* qkv, const int32_t* slot_map, uint16_t* q,
-                                long long q_stride, uint16_t* k_cache, uint16_t* v_cache, cudaStream_t st);
+// `used`: device word with the rows in use, null = all of them.
+cudaError_t launch_paged_append(const moe_paged_shape_t& s, const uint16_t* qkv, const int32_t* slot_map,
+                                const int32_t* used, uint16_t* q, long long q_stride, uint16_t* k_cache,
+                                uint16_t* v_cache, cudaStream_t st);
 size_t paged_attention_scratch_bytes(const moe_paged_shape_t& s);
 cudaError_t launch_paged_attention(const moe_paged_shape_t& s, const uint16_t* q, long long q_stride,
                                    const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* block_table,

@@ -86,9 +86,10 @@ moe_status_t moe_paged_append(const moe_paged_shape_t* shape, const void* qkv, c
   // In place the rows have to be the projection's own.
   if (q == qkv && q_stride_of(shape) != (long long)(shape->n_head + 2 * shape->n_kv_head) * kAttnHeadDim)
     return MOE_ERR_INVALID_ARG;
-  return status_of(launch_paged_append(*shape, static_cast<const uint16_t*>(qkv), slot_map, static_cast<uint16_t*>(q),
-                                       q_stride_of(shape), static_cast<uint16_t*>(k_cache),
-                                       static_cast<uint16_t*>(v_cache), static_cast<cudaStream_t>(stream)));
+  return status_of(launch_paged_append(*shape, static_cast<const uint16_t*>(qkv), slot_map, nullptr,
+                                       static_cast<uint16_t*>(q), q_stride_of(shape),
+                                       static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache),
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_paged_attention_workspace_size(const moe_paged_shape_t* shape) {
@@ -140,10 +141,11 @@ moe_status_t moe_attention_paged_fwd(const moe_paged_shape_t* shape, int32_t d, 
   const GemmOperandSet proj{x, T, w_qkv, 1, C, d, qkv, C, EPI_STORE, T};
   cudaError_t e = launch_grouped_gemm(off, nullptr, 1, proj, none, 0, s, &bad);
   if (bad) return MOE_ERR_UNSUPPORTED;
-  // The query heads are normalised where the projection left them.
+  // The query heads are normalised where the projection left them.  Rows past the plan's write
+  // no cache: a slot map that a larger step has filled holds live slots there.
   if (e == cudaSuccess)
-    e = launch_paged_append(*shape, qkv, slot_map, qkv, C, static_cast<uint16_t*>(k_cache),
-                            static_cast<uint16_t*>(v_cache), s);
+    e = launch_paged_append(*shape, qkv, slot_map, row_start + shape->requests, qkv, C,
+                            static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache), s);
   if (e == cudaSuccess)
     e = launch_paged_attention(*shape, qkv, C, static_cast<const uint16_t*>(k_cache),
                                static_cast<const uint16_t*>(v_cache), block_table, row_start, kv_len, o, nullptr,

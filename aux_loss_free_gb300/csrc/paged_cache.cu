@@ -234,6 +234,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 struct AppendParams {
   const uint16_t* qkv;
   const int32_t* slot_map;
+  const int32_t* used;  // rows in use: the others have no slot, whatever the map holds there; null = all rows
   uint16_t* q;
   uint16_t* k_cache;
   uint16_t* v_cache;
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(256, 4) paged_append_kernel(const AppendParams
   if (t >= p.T) return;
   const int heads = p.n_head + 2 * p.n_kv_head;
   const uint4* src = reinterpret_cast<const uint4*>(p.qkv + (long long)t * heads * HD) + col;
-  const int slot = p.slot_map[t];
+  const int used = p.used ? *p.used : p.T, mapped = p.slot_map[t], slot = t < used ? mapped : -1;
   const bool kept = slot >= 0 && slot < p.slots;
   const int last = kept ? heads : p.n_head;  // a row without a slot has its query heads alone moved
   const long long page = kept ? slot >> p.page_shift : 0;
@@ -326,9 +327,10 @@ cudaError_t launch_paged_plan(const moe_paged_shape_t& s, const int32_t* ctx_len
   return launch_pdl(paged_plan_kernel, dim3((unsigned)blocks), dim3(PLAN_THREADS), smem, st, p);
 }
 
-cudaError_t launch_paged_append(const moe_paged_shape_t& s, const uint16_t* qkv, const int32_t* slot_map, uint16_t* q,
-                                long long q_stride, uint16_t* k_cache, uint16_t* v_cache, cudaStream_t st) {
-  const AppendParams p{qkv, slot_map, q, k_cache, v_cache, q_stride, s.tokens, s.n_head, s.n_kv_head,
+cudaError_t launch_paged_append(const moe_paged_shape_t& s, const uint16_t* qkv, const int32_t* slot_map,
+                                const int32_t* used, uint16_t* q, long long q_stride, uint16_t* k_cache,
+                                uint16_t* v_cache, cudaStream_t st) {
+  const AppendParams p{qkv, slot_map, used, q, k_cache, v_cache, q_stride, s.tokens, s.n_head, s.n_kv_head,
                        log2_of(s.page_size), s.pages * s.page_size, s.eps};
   return launch_pdl(paged_append_kernel, dim3((unsigned)((s.tokens + 7) / 8)), dim3(256), 0, st, p);
 }

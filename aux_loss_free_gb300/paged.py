@@ -27,6 +27,7 @@ class PagedStep:
         dev = torch.device(device)
         self.requests, self.pages, self.page_size, self.max_pages = requests, pages, page_size, max_pages
         self.max_tokens = max_tokens
+        self.tokens = 0  # rows of the step that was planned (or captured) last
 
         def i32(*shape):
             return torch.zeros(*shape, dtype=torch.int32, device=dev)
@@ -68,6 +69,7 @@ class PagedStep:
         else:
             with torch.cuda.stream(stream):
                 now.copy_(after)
+        self.tokens = tokens
         return self
 
 
@@ -87,8 +89,10 @@ class PagedAttention:
         self.workspace = torch.empty(n, dtype=torch.uint8, device=w_qkv.device)
 
     def forward(self, x: torch.Tensor, out: torch.Tensor, residual: bool = True, stream=None) -> torch.Tensor:
-        """x, out [tokens][d] bf16: the rows of the step that was planned last."""
+        """x, out [tokens][d] bf16: the rows of the step that was planned last, all of them."""
         st = self.step
+        if x.shape[0] != st.tokens or out.shape[0] != st.tokens:
+            raise ValueError(f"x has {x.shape[0]} rows and out {out.shape[0]}, the planned step {st.tokens}")
         L.moe_attention_paged_fwd(st.shape(x.shape[0], self.n_head, self.n_kv_head, self.eps), self.d, x, self.w_qkv,
                                   self.w_o, residual, self.k_cache, self.v_cache, st.block_table, st.row_start,
                                   st.slot_map, st.kv_len, out, self.workspace, stream=stream)

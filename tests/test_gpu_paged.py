@@ -656,3 +656,38 @@ def test_a_captured_step_goes_on_where_the_last_one_ended():
     assert sorted(seqs) == ["a", "b", "b'", "c"]
     for name, parts in seqs.items():
         assert_close_bf16(np.concatenate(got[name]), _dense(np.concatenate(parts), w, a), f"sequence {name}")
+
+
+def test_rows_past_the_planned_step_write_no_cache():
+    """A large step, then a small one: the slot map still holds the large step's slots behind
+    the small one's rows.  The class refuses a batch of another size; the C call takes the rows
+    past the plan as padding and leaves every other token's keys and values as they are."""
+    a = ATTN_CONFIGS["attn_tiny"].replace(batch=1, seq=64, n_head=8, n_kv_head=2, d=512)
+    H = make_attention(a, "attn_tiny")
+    w_qkv = to_device_bf16(np.concatenate([H["w_q"], H["w_k"], H["w_v"]], axis=0), DEV)
+    step = PagedStep(requests=2, pages=12, page_size=16, max_pages=6, max_tokens=64)
+    block = PagedAttention(step, a.d, 8, 2, w_qkv, to_device_bf16(H["w_o"], DEV), a.eps)
+    block.k_cache.zero_()
+    block.v_cache.zero_()
+    rng = np.random.default_rng(33)
+    x = _rows(rng, 60, a.d)
+    out = torch.empty_like(x)
+    with pytest.raises(ValueError):
+        block.forward(x, out)  # nothing is planned yet
+    step.plan(_i32([40, 20]), 60)
+    block.forward(x, out)
+    step.plan(_i32([1, 1]), 2)
+    y = _rows(rng, 60, a.d)
+    for rows, to in ((y, out), (y[:2], out), (y, out[:2]), (y[:1], out[:1])):
+        with pytest.raises(ValueError):
+            block.forward(rows, to)
+    slots = step.slot_map[:2].tolist()
+    k, v = block.k_cache.clone(), block.v_cache.clone()
+    M.moe_attention_paged_fwd(step.shape(60, 8, 2, a.eps), a.d, y, block.w_qkv, block.w_o, True, block.k_cache,
+                              block.v_cache, step.block_table, step.row_start, step.slot_map, step.kv_len, out,
+                              block.workspace)
+    torch.cuda.synchronize()
+    assert torch.equal(out[2:], y[2:])  # padding rows
+    for cache, was in ((block.k_cache, k), (block.v_cache, v)):
+        changed = (cache != was).any(dim=3).any(dim=1).flatten().nonzero().flatten().tolist()
+        assert changed == sorted(slots)
