@@ -14,6 +14,23 @@ import torch
 from . import _lib as L
 
 
+def _check(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device: torch.device):
+    """The library gets addresses alone: what it finds there is checked here."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: type {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: size {list(t.shape)}, not {list(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous (strides {list(t.stride())})")
+    if t.device != device:
+        raise ValueError(f"{name}: on device {t.device}, not {device}")
+
+
+def _check_cuda(device: torch.device):
+    if device.type != "cuda":
+        raise ValueError(f"the calls run on a CUDA device, not on {device}")
+
+
 class PagedStep:
     """Block tables, page pool and lengths of up to `requests` requests at a time.
 
@@ -54,7 +71,7 @@ class PagedStep:
 
     def shape(self, tokens: int, n_head: int = 1, n_kv_head: int = 1, eps: float = 1e-6):
         if tokens > self.max_tokens:
-            raise ValueError(f"{tokens} rows in a step planned for at most {self.max_tokens}")
+            raise ValueError(f"{tokens} rows in a step made for at most {self.max_tokens}")
         return L.make_paged_shape(self.requests, tokens, n_head, n_kv_head, self.page_size, self.pages, self.max_pages,
                                   eps=eps)
 
@@ -62,6 +79,8 @@ class PagedStep:
         """One step of `tokens` rows: new_len [requests] int32 (device): new tokens per request,
         0 = none, -1 = ended.  Rows past their sum are padding."""
         now, after = self._now, self._next
+        _check("new_len", new_len, torch.int32, (self.requests,), now.device)
+        _check_cuda(now.device)
         L.moe_paged_plan(self.shape(tokens), now[4:], new_len, self.block_table, self.pool, now, after,
                          self.row_start, self.slot_map, self.kv_len, after[4:], self.info, stream=stream)
         if stream is None:
@@ -79,20 +98,25 @@ class PagedAttention:
     def __init__(self, step: PagedStep, d: int, n_head: int, n_kv_head: int, w_qkv: torch.Tensor, w_o: torch.Tensor,
                  eps: float = 1e-6):
         self.step, self.d, self.n_head, self.n_kv_head, self.eps = step, d, n_head, n_kv_head, eps
+        dev = step.block_table.device
+        _check("w_qkv", w_qkv, torch.bfloat16, ((n_head + 2 * n_kv_head) * 128, d), dev)
+        _check("w_o", w_o, torch.bfloat16, (d, n_head * 128), dev)
         self.w_qkv, self.w_o = w_qkv, w_o
         cache = (step.pages, n_kv_head, step.page_size, 128)
-        self.k_cache = torch.empty(cache, dtype=torch.bfloat16, device=w_qkv.device)
-        self.v_cache = torch.empty(cache, dtype=torch.bfloat16, device=w_qkv.device)
+        self.k_cache = torch.empty(cache, dtype=torch.bfloat16, device=dev)
+        self.v_cache = torch.empty(cache, dtype=torch.bfloat16, device=dev)
         n = L.moe_attention_paged_workspace_size(step.shape(step.max_tokens, n_head, n_kv_head, eps), d)
         if n == 0:
             raise L.MoEError("moe_attention_paged_workspace_size", 2)
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=w_qkv.device)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
 
     def forward(self, x: torch.Tensor, out: torch.Tensor, residual: bool = True, stream=None) -> torch.Tensor:
         """x, out [tokens][d] bf16: the rows of the step that was planned last, all of them."""
         st = self.step
-        if x.shape[0] != st.tokens or out.shape[0] != st.tokens:
-            raise ValueError(f"x has {x.shape[0]} rows and out {out.shape[0]}, the planned step {st.tokens}")
+        rows = (st.tokens, self.d)
+        _check("x", x, torch.bfloat16, rows, self.w_qkv.device)
+        _check("out", out, torch.bfloat16, rows, self.w_qkv.device)
+        _check_cuda(self.w_qkv.device)
         L.moe_attention_paged_fwd(st.shape(x.shape[0], self.n_head, self.n_kv_head, self.eps), self.d, x, self.w_qkv,
                                   self.w_o, residual, self.k_cache, self.v_cache, st.block_table, st.row_start,
                                   st.slot_map, st.kv_len, out, self.workspace, stream=stream)

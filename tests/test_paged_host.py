@@ -5,9 +5,11 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import aux_loss_free_gb300 as M
 from aux_loss_free_gb300 import build as B
+from aux_loss_free_gb300 import paged
 from oracle import attention_oracle as A
 from oracle import paged_oracle as P
 
@@ -105,3 +107,74 @@ def test_paged_attention_oracle_equals_the_dense_oracle():
     for a, b in ((0, 30), (30, 45)):
         got = P.paged_attention(q[a:b], kc, vc, ids[None], np.array([0, b - a]), np.array([b]), H, KV)
         np.testing.assert_allclose(got["out"], r["o"][a:b], rtol=1e-10, atol=1e-12)
+
+
+
+@pytest.fixture
+def step(lib, monkeypatch):
+    """A step of two requests whose tensors lie on the host; a call that gets past the checks
+    fails the test instead of passing host addresses on."""
+    def reached(*_, **__):
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(paged.L, "moe_paged_plan", reached)
+    monkeypatch.setattr(paged.L, "moe_attention_paged_fwd", reached)
+    return paged.PagedStep(requests=2, pages=4, page_size=16, max_pages=2, max_tokens=8, device="cpu")
+
+
+NEW_LEN = {  # of two requests, and what the refusal says
+    "int64": (lambda: torch.tensor([1, 1]), "type"),
+    "float": (lambda: torch.tensor([1.0, 1.0]), "type"),
+    "too-few": (lambda: torch.tensor([1], dtype=torch.int32), "size"),
+    "too-many": (lambda: torch.tensor([1, 1, 1], dtype=torch.int32), "size"),
+    "two-dims": (lambda: torch.tensor([[1, 1]], dtype=torch.int32), "size"),
+    "strided": (lambda: torch.tensor([1, 7, 1, 7], dtype=torch.int32)[::2], "contiguous"),
+    "elsewhere": (lambda: torch.empty(2, dtype=torch.int32, device="meta"), "device"),
+    "on-the-host": (lambda: torch.tensor([1, 1], dtype=torch.int32), "CUDA device"),
+}
+
+
+@pytest.mark.parametrize("name", NEW_LEN)
+def test_plan_refuses_other_tensors(step, name):
+    make, why = NEW_LEN[name]
+    with pytest.raises(ValueError, match=why):
+        step.plan(make(), 2)
+    assert step.tokens == 0
+
+
+def _block(step, w_qkv=(512, 64), w_o=(64, 256), dtype=torch.bfloat16):
+    return paged.PagedAttention(step, 64, 2, 1, torch.zeros(w_qkv, dtype=dtype), torch.zeros(w_o, dtype=dtype))
+
+
+@pytest.mark.parametrize("change,why", [(dict(w_qkv=(511, 64)), "w_qkv: size"), (dict(w_qkv=(512, 128)), "w_qkv: size"),
+                                        (dict(w_o=(256, 64)), "w_o: size"), (dict(w_o=(64, 128)), "w_o: size"),
+                                        (dict(dtype=torch.float32), "w_qkv: type")], ids=str)
+def test_the_block_refuses_other_weights(step, change, why):
+    with pytest.raises(ValueError, match=why):
+        _block(step, **change)
+
+
+ROWS = {  # of a step of 4 rows, width 64
+    "float32": (lambda: torch.zeros(4, 64), "type"),
+    "too-few": (lambda: torch.zeros(3, 64, dtype=torch.bfloat16), "size"),
+    "too-many": (lambda: torch.zeros(5, 64, dtype=torch.bfloat16), "size"),
+    "wide": (lambda: torch.zeros(4, 128, dtype=torch.bfloat16), "size"),
+    "three-dims": (lambda: torch.zeros(1, 4, 64, dtype=torch.bfloat16), "size"),
+    "columns-of-wider-rows": (lambda: torch.zeros(4, 128, dtype=torch.bfloat16)[:, :64], "contiguous"),
+    "transposed": (lambda: torch.zeros(64, 4, dtype=torch.bfloat16).t(), "contiguous"),
+    "elsewhere": (lambda: torch.empty(4, 64, dtype=torch.bfloat16, device="meta"), "device"),
+}
+
+
+@pytest.mark.parametrize("name", ROWS)
+@pytest.mark.parametrize("which", ["x", "out"])
+def test_the_block_refuses_other_rows(step, name, which):
+    block, good = _block(step), torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x: size"):  # nothing is planned yet
+        block.forward(good, good)
+    step.tokens = 4
+    make, why = ROWS[name]
+    with pytest.raises(ValueError, match=f"{which}: .*{why}"):
+        block.forward(*((make(), good) if which == "x" else (good, make())))
+    with pytest.raises(ValueError, match="CUDA device"):
+        block.forward(good, good)
