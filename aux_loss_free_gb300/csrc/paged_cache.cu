@@ -40,8 +40,9 @@ struct PlanParams {
   const int32_t* new_len;
   int32_t* table;
   int32_t* pool;
-  const int32_t* pool_in;
-  int32_t* pool_out;
+  const int32_t* pool_in;  // with one CTA pool_out may be pool_in, next_ctx ctx_len: both are read
+  int32_t* pool_out;       // ahead of the first barrier and written behind it.  Null: left to
+                           // paged_advance_kernel
   int32_t* row_start;
   int32_t* slot_map;
   int32_t* kv_len;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
     if (first_cta) {
       p.row_start[r] = s_row[r];
       p.kv_len[r] = granted ? c + n : n == 0 ? c : 0;
-      p.next_ctx[r] = granted ? c + n : n < 0 ? 0 : c;
+      if (p.next_ctx) p.next_ctx[r] = granted ? c + n : n < 0 ? 0 : c;
     }
   }
   const int used = (int)min(all_rows, (long long)p.T), returned = (int)min(all_back, (long long)p.pages);
@@ -182,8 +183,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
       // No more than `pages` pages are free: a caller that returns a page twice is told so.
       if (count + all_back > p.pages) bad = true;
       p.row_start[p.R] = used;
-      p.pool_out[0] = (int)(((long long)head + s_taken) % p.pages);
-      p.pool_out[1] = (int)min(count - s_taken + all_back, (long long)p.pages);
+      if (p.pool_out) {
+        p.pool_out[0] = (int)(((long long)head + s_taken) % p.pages);
+        p.pool_out[1] = (int)min(count - s_taken + all_back, (long long)p.pages);
+      }
       p.info[0] = used;
       p.info[1] = s_taken;
       p.info[2] = returned;
@@ -224,6 +227,29 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
     p.pool[ring(count + k)] = p.table[(long long)r * p.max_pages + (k - s_back[r])];
   }
   if (bad) atomicOr(p.status, kDevCheck);
+}
+
+// A step in place that several CTAs plan: the contexts and the pool's state are replaced by a
+// launch of its own, once every CTA of the plan has read them.  What it needs is among the plan's
+// outputs: a request's next context is its kv_len, but 0 if it ended and the present one if it was
+// denied (new tokens and no keys).
+__global__ void __launch_bounds__(PLAN_THREADS) paged_advance_kernel(int32_t* ctx, const int32_t* new_len,
+                                                                     const int32_t* kv_len, int32_t* pool_state,
+                                                                     const int32_t* info, int R, int pages) {
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x * PLAN_THREADS + threadIdx.x;
+  if (ctx && r < R) {
+    const int n = new_len[r], kv = kv_len[r];
+    if (n < 0) ctx[r] = 0;
+    else if (n > 0 && kv > 0) ctx[r] = kv;
+  }
+  if (pool_state && r == 0) {
+    const int head = pool_state[0], count = pool_state[1], taken = info[1], returned = info[2];
+    const bool ok = head >= 0 && head < pages && count >= 0 && count <= pages;  // else nothing was taken
+    pool_state[0] = ok ? (int)(((long long)head + taken) % pages) : 0;
+    pool_state[1] = (int)min((ok ? count - taken : 0) + (long long)returned, (long long)pages);
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -312,8 +338,14 @@ cudaError_t launch_paged_plan(const moe_paged_shape_t& s, const int32_t* ctx_len
                               int32_t* block_table, int32_t* pool, const int32_t* pool_in, int32_t* pool_out,
                               int32_t* row_start, int32_t* slot_map, int32_t* kv_len, int32_t* next_ctx, int32_t* info,
                               cudaStream_t st) {
-  PlanParams p{ctx_len, new_len, block_table, pool, pool_in, pool_out, row_start, slot_map, kv_len, next_ctx, info,
-               device_status_ptr(), s.requests, s.tokens, s.pages, s.max_pages, log2_of(s.page_size)};
+  // Enough threads for the rows, and for an eighth of the tables' pages coming back at once.
+  const long long work = std::max<long long>(s.tokens, (long long)s.requests * s.max_pages / 8);
+  const long long blocks = std::min<long long>((work + PLAN_THREADS - 1) / PLAN_THREADS, 152);
+  int32_t* const ctx_late = blocks > 1 && next_ctx == ctx_len ? next_ctx : nullptr;
+  int32_t* const pool_late = blocks > 1 && pool_out == pool_in ? pool_out : nullptr;
+  PlanParams p{ctx_len, new_len, block_table, pool, pool_in, pool_late ? nullptr : pool_out, row_start, slot_map,
+               kv_len, ctx_late ? nullptr : next_ctx, info, device_status_ptr(), s.requests, s.tokens, s.pages,
+               s.max_pages, log2_of(s.page_size)};
   if (!p.status) return cudaErrorInvalidDevicePointer;
   const size_t smem = sizeof(int32_t) * (4 * (size_t)s.requests + 2);
   if (smem > 48 * 1024) {
@@ -321,10 +353,11 @@ cudaError_t launch_paged_plan(const moe_paged_shape_t& s, const int32_t* ctx_len
                                                (int)(sizeof(int32_t) * (4 * kPagedMaxRequests + 2)));
     if (e != cudaSuccess) return e;
   }
-  // Enough threads for the rows, and for an eighth of the tables' pages coming back at once.
-  const long long work = std::max<long long>(s.tokens, (long long)s.requests * s.max_pages / 8);
-  const long long blocks = std::min<long long>((work + PLAN_THREADS - 1) / PLAN_THREADS, 152);
-  return launch_pdl(paged_plan_kernel, dim3((unsigned)blocks), dim3(PLAN_THREADS), smem, st, p);
+  const cudaError_t e = launch_pdl(paged_plan_kernel, dim3((unsigned)blocks), dim3(PLAN_THREADS), smem, st, p);
+  if (e != cudaSuccess || (!ctx_late && !pool_late)) return e;
+  const unsigned rows = ctx_late ? (unsigned)s.requests : 1u;
+  return launch_pdl(paged_advance_kernel, dim3((rows + PLAN_THREADS - 1) / PLAN_THREADS), dim3(PLAN_THREADS), 0, st,
+                    ctx_late, new_len, (const int32_t*)kv_len, pool_late, (const int32_t*)info, s.requests, s.pages);
 }
 
 cudaError_t launch_paged_append(const moe_paged_shape_t& s, const uint16_t* qkv, const int32_t* slot_map,

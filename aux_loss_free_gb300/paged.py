@@ -2,10 +2,9 @@
 attention block's cache and weights.
 
 PyTorch provides the device memory; every computation runs in the library
-(moe_paged_plan, moe_attention_paged_fwd).  `PagedStep.plan` is one moe_paged_plan call and a
-copy of its next lengths over the present ones, `PagedAttention.forward` one
-moe_attention_paged_fwd call; neither waits for the GPU, and both can be captured and
-replayed with other lengths.
+(moe_paged_plan, moe_attention_paged_fwd).  `PagedStep.plan` is one moe_paged_plan call,
+`PagedAttention.forward` one moe_attention_paged_fwd call; neither waits for the GPU, and
+both can be captured and replayed with other lengths.
 """
 from __future__ import annotations
 
@@ -51,23 +50,20 @@ class PagedStep:
 
         self.block_table = torch.full((requests, max_pages), -1, dtype=torch.int32, device=dev)
         self.pool = torch.arange(pages, dtype=torch.int32, device=dev)
-        # The pool's state (two words of four) and the context lengths before a step and after it.
-        # Every plan reads the first and writes the second, which then replaces the first in stream
-        # order: the addresses of all steps are the same, so that a captured plan goes on from where
-        # the last step or replay ended.
-        self._now, self._next = i32(4 + requests), i32(4 + requests)
-        self._now[1] = pages
+        # Every plan takes these in place, so that a captured one goes on from where the last step
+        # or replay ended.
+        self._ctx, self._state = i32(requests), torch.tensor([0, pages], dtype=torch.int32, device=dev)
         self.row_start, self.slot_map, self.kv_len, self.info = i32(requests + 1), i32(max_tokens), i32(requests), i32(4)
 
     @property
     def ctx_len(self) -> torch.Tensor:
         """[requests] int32: the tokens that every request has in the cache."""
-        return self._now[4:]
+        return self._ctx
 
     @property
     def free_pages(self) -> torch.Tensor:
         """[1] int32: pages in the pool."""
-        return self._now[1:2]
+        return self._state[1:]
 
     def shape(self, tokens: int, n_head: int = 1, n_kv_head: int = 1, eps: float = 1e-6):
         if tokens > self.max_tokens:
@@ -78,16 +74,11 @@ class PagedStep:
     def plan(self, new_len: torch.Tensor, tokens: int, stream=None) -> "PagedStep":
         """One step of `tokens` rows: new_len [requests] int32 (device): new tokens per request,
         0 = none, -1 = ended.  Rows past their sum are padding."""
-        now, after = self._now, self._next
-        _check("new_len", new_len, torch.int32, (self.requests,), now.device)
-        _check_cuda(now.device)
-        L.moe_paged_plan(self.shape(tokens), now[4:], new_len, self.block_table, self.pool, now, after,
-                         self.row_start, self.slot_map, self.kv_len, after[4:], self.info, stream=stream)
-        if stream is None:
-            now.copy_(after)
-        else:
-            with torch.cuda.stream(stream):
-                now.copy_(after)
+        ctx, state = self._ctx, self._state
+        _check("new_len", new_len, torch.int32, (self.requests,), ctx.device)
+        _check_cuda(ctx.device)
+        L.moe_paged_plan(self.shape(tokens), ctx, new_len, self.block_table, self.pool, state, state, self.row_start,
+                         self.slot_map, self.kv_len, ctx, self.info, stream=stream)
         self.tokens = tokens
         return self
 

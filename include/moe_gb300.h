@@ -442,8 +442,11 @@ typedef struct {
  * does not fit: ctx_len outside [0, max_pages * page_size], more than max_pages pages, rows
  * past T.  A request that does not fit asks for no page; that, a pool state outside
  * [0, pages) x [0, pages] and a table entry in use that is no page set MOE_ERR_DEVICE in the
- * device status word.  No input but block_table and pool may overlap an output; the outputs
- * depend on the inputs alone, so the call can be repeated on the same inputs. */
+ * device status word.  The outputs depend on the inputs alone, so the call can be repeated on
+ * the same inputs; no input but block_table and pool overlaps an output, except that a step
+ * can be taken in place: next_ctx == ctx_len and pool_state_out == pool_state_in (either or
+ * both) replace the present lengths and pool state by the next ones, and a captured call then
+ * goes on from step to step. */
 moe_status_t moe_paged_plan(const moe_paged_shape_t* shape, const int32_t* ctx_len, const int32_t* new_len,
                             int32_t* block_table, int32_t* pool, const int32_t* pool_state_in,
                             int32_t* pool_state_out, int32_t* row_start, int32_t* slot_map, int32_t* kv_len,

@@ -691,3 +691,35 @@ def test_rows_past_the_planned_step_write_no_cache():
     for cache, was in ((block.k_cache, k), (block.v_cache, v)):
         changed = (cache != was).any(dim=3).any(dim=1).flatten().nonzero().flatten().tolist()
         assert changed == sorted(slots)
+
+
+@pytest.mark.parametrize("R,max_pages,pad", [(1, 4, 0), (8, 20, 2), (40, 30, 3), (700, 12, 1), (4096, 6, 0)])
+@pytest.mark.parametrize("which", ["both", "ctx", "pool"])
+def test_plan_in_place(R, max_pages, pad, which):
+    """next_ctx over ctx_len and pool_state_out over pool_state_in, with one CTA and with many:
+    the oracle's outputs, step after step from the lengths that the last one left."""
+    rng = np.random.default_rng(R + pad)
+    choices = [-1, 0, 1, 1, 5, 17, 40]
+    s = _random_step(rng, R, 16, max_pages, rng.choice(choices, size=R), free=R // 20 + 1)
+    T = s["tokens"] = max(s["tokens"], 4 * R) + pad
+    shape = M.make_paged_shape(R, T, 8, 2, 16, s["pages"], max_pages)
+    ctx, state, table, pool = _i32(s["ctx"]), _i32(s["state"]), _i32(s["table"]), _i32(s["pool"])
+    nxt, after = (ctx if which != "pool" else torch.empty_like(ctx)), (state if which != "ctx" else _i32([7, 7]))
+    rs, slot, kv, info = _i32([0] * (R + 1)), _i32([0] * T), _i32([0] * R), _i32([0] * 4)
+    denied = 0
+    for _ in range(4):
+        ref = P.step_plan(s["ctx"], s["new"], s["table"], s["pool"], s["state"], T, s["pages"], 16)
+        M.moe_paged_plan(shape, ctx, _i32(s["new"]), table, pool, state, after, rs, slot, kv, nxt, info)
+        torch.cuda.synchronize()
+        got = dict(block_table=table, pool=pool, row_start=rs, slot_map=slot, kv_len=kv, next_ctx=nxt,
+                   pool_state=after, info=info)
+        for k, v in ref.items():
+            assert np.array_equal(got[k].cpu().numpy(), v), k
+        denied += ref["info"][3]
+        ctx.copy_(nxt)
+        state.copy_(after)
+        s.update(ctx=ref["next_ctx"], table=ref["block_table"], pool=ref["pool"], state=ref["pool_state"])
+        room = np.minimum(rng.choice(choices, size=R), max_pages * 16 - s["ctx"])
+        s["new"] = np.where(np.cumsum(np.maximum(room, 0)) <= T, room, 0)
+    assert denied or R < 700  # the pool runs short in the larger ones
+    assert M.moe_device_status() == 0
