@@ -42,8 +42,15 @@
 //     rescaled only when a row's maximum grew by more than 8 (2^8); at the end O / l, or O, m
 //     and l as a partial.  The weights are rounded to bf16, the tensor cores' type beside bf16
 //     values; scores, maxima, sums and O stay in fp32, and so do the partials.
-// Values past the last key that a tile may see are zeroed in shared memory before P V: their
-// weight is 0, but 0 times a stale NaN or infinity is not.
+// A key that a row does not see has weight 0, but 0 times a NaN or an infinity is not 0.  Values
+// past the last key of a work tile are therefore zeroed in shared memory before P V; those that
+// its later rows see and its first row does not (as many keys as the tile has tokens, less one) are
+// looked through, and a NaN or an infinity among them is taken out and added, at the end, to the
+// rows that see it.  Both while the tile's scores are computed, so that it costs little: without
+// and with the search four 2048-token prompts took 44.05 and 44.15 us, 13 x 5 tokens 15.2 and 15.7,
+// one token over 2047 keys 11.8 and 11.9, over 131070 33.4 and 34.2 (each instruction that a launch
+// reaches is fetched anew, so the loops stay rolled: all unrolled 16.0, 12.1 and 34.2; the search
+// rolled whole, one 16-byte chunk a turn, takes the prompts to 45.1).
 // Every wait for a copy, a product or another CTA is bounded; on a timeout the status word is set
 // and the CTA exits.  The issuer's waits for the parts of P are hardware barriers without a limit:
 // a half that has an item arrives at every one of them, whatever became of its own waits.
@@ -78,7 +85,7 @@ constexpr int TILE_BYTES = 2 * ATOM_BYTES;    // 32 KB: 128 rows x 128
 constexpr int STAGES = 5;                     // key and value tiles in flight: K0 V0 K1 V1 ...
 constexpr int RING_OFF = 2 * TILE_BYTES;      // after the two query halves
 constexpr int STATE_OFF = RING_OFF + STAGES * TILE_BYTES;
-constexpr int SMEM_BYTES = STATE_OFF + 1024;
+constexpr int SMEM_BYTES = STATE_OFF + 3072;
 constexpr int SOFTMAX_WARPS = 16;             // eight per query half, 16 rows each
 constexpr int LOAD_WARP = 16, MMA_WARP = 17;
 constexpr int THREADS = 576;
@@ -134,6 +141,7 @@ struct Item {
   int g, half;      // key/value head; query half of a single tile, 2 = pair
   int part;         // partial slot to write; -1 = none: the whole work tile, or the part that adds the others
   int added;        // parts that the first CTA adds to its own; 0 = none
+  int late;         // whether a late value is no number (SmemState::late)
 };
 
 // One request's work tiles.
@@ -214,6 +222,10 @@ struct SmemState {
   uint64_t o_full[2];
   uint64_t item_full[ITEMS], item_empty[ITEMS];
   Item items[ITEMS];
+  // Of an item and column, the first of the values that only some rows of the work tile see and
+  // that are NaN (byte 0), +inf (1), -inf (2): 256 less its position after the tile's first token;
+  // 0: none.
+  alignas(16) uint32_t late[ITEMS][HD];
   long long warp_sum[WARPS];
   long long start_off;   // units of the starting request before the range
   int start_req;
@@ -383,6 +395,57 @@ __device__ __forceinline__ void tmem_st_pairs4(uint32_t taddr, const uint32_t (&
       "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
+}
+
+// Whether one of two bf16 (of eight) has the exponent of NaN and infinity, in bits 15 and 31.
+__device__ __forceinline__ uint32_t no_number(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+__device__ __forceinline__ bool no_number(const uint4& v) {
+  return ((no_number(v.x) | no_number(v.y) | no_number(v.z) | no_number(v.w)) & 0x80008000u) != 0;
+}
+// Takes what is no number out of half a value row in shared memory (64 columns from `col0` on, 16-byte
+// chunks xor `swizzle`) and notes it under `mark`, 256 less the row's position after the work tile's
+// first token.  The note is there before the value is gone: a thread of the other query half that
+// finds the row clean finds the note.
+__device__ __noinline__ void take_out(uint4* row, int swizzle, int col0, uint32_t mark, uint32_t* late, int* any) {
+  *any = 1;
+  for (int c = 0; c < 8; ++c) {
+    uint4 v = row[c];
+    if (!no_number(v)) continue;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = w[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+      if ((h & 0x7F80u) != 0x7F80u) continue;
+      const uint32_t note = mark << (h & 0x7Fu ? 0 : h >> 15 ? 16 : 8);
+      uint32_t* const at = late + col0 + ((c ^ swizzle) << 3) + e;
+      // The larger of each byte; a turn that fails means that another thread raised one.
+      for (uint32_t was = *(volatile uint32_t*)at, old; (old = atomicCAS(at, was, __vmaxu4(was, note))) != was; was = old) {
+      }
+      w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+    __threadfence_block();
+    row[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// Adds the values taken out to the warp's rows (`tok`: their tokens in the work tile) that see them.
+__device__ __noinline__ void add_late(const uint32_t* late, uint32_t ocol, int tok0, int tok1) {
+  for (int y = 0; y < HD / 32; ++y) {
+    uint32_t o[16];
+    tmem_ld_quad4(ocol + 32 * y, o);
+    tmem_wait_quad4(o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t n = late[32 * y + (i >> 2) * 8 + (threadIdx.x & 3) * 2 + (i & 1)];
+      const uint32_t tok = i & 2 ? tok1 : tok0;
+      const bool nan = (n & 0xFFu) + tok >= 256, up = (n >> 8 & 0xFFu) + tok >= 256, down = (n >> 16) + tok >= 256;
+      if (nan || up || down) {
+        const float v = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+        o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+      }
+    }
+    __syncwarp();
+    tmem_st_quad4(ocol + 32 * y, o);
+  }
+  tmem_wait_st();
 }
 
 __device__ __forceinline__ float quad_max(float x) {
@@ -591,6 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       it.j0 = j;
       it.nt = min(units, tile_n - j);  // the units past the key tiles hold no work
       it.g = g;
+      it.late = 0;
       if (it.nt > 0) {
         // Page ids of the first key tile.
         const int32_t* const row = p.table + (long long)r * p.max_pages;
@@ -651,6 +715,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               const int slot = items % ITEMS;
               ok = warp_wait(&sm.item_empty[slot], (items / ITEMS) ^ 1u, p.status);
               if (!ok) break;
+              reinterpret_cast<uint4*>(sm.late[slot])[lane] = make_uint4(0, 0, 0, 0);
+              __syncwarp();
               if (lane == 0) {
                 sm.items[slot] = it;
                 mbar_arrive(smem_u32(&sm.item_full[slot]));
@@ -858,6 +924,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         continue;
       }
       const int kvlim = it.kvlim, first_key = it.j0 * BK;
+      const int all_see = min(it.pos0 + 1, kvlim);  // keys that every row of the work tile sees
       // Keys that this lane's rows (lane0 + lane / 4 and eight further) see; a row that is not
       // stored needs no mask.
       int limit[2];
@@ -877,26 +944,37 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         const int sb = pair ? wg : 2 + b;            // barrier set
         const uint32_t scol = tl + (pair ? wg : b) * BK;
         const uint32_t ph = pair ? pairs + t : (b ? odd : even) + (t >> 1);
+        const int k0 = first_key + t * BK;
+        if (k0 + BK > all_see) {
+          // Values that some row of the tile does not see: rows all_see - k0 .. 127 of the stage, no
+          // row from kvlim - k0 on.  While the tile's scores are computed.
+          const uint32_t vl = 2 * (tiles + t) + 1;
+          half_wait(&sm.ring_full[vl % STAGES], vl / STAGES, wg, p.status, nullptr);
+          const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
+          if (zrow >= all_see - k0) {  // chunk x + zrow: eight rows of a warp take eight bank groups
+            uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + (zrow >> 3) * 2048 +
+                                                      zcol * 1024 + (zrow & 7) * 128);
+            if (zrow >= kvlim - k0) {
+#pragma unroll 1
+              for (int x = 0; x < 8; ++x) z[(x + zrow) & 7] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            } else {
+              bool found = false;
+#pragma unroll 4
+              for (int x = 0; x < 8; ++x) found |= no_number(z[(x + zrow) & 7]);
+              if (__builtin_expect(found, 0)) {
+                take_out(z, zrow & 7, 64 * zcol, 256 - (k0 + zrow - it.pos0), sm.late[slot], &sm.items[slot].late);
+                fence_proxy_async_smem();
+              }
+            }
+          }
+          __syncwarp();
+        }
         if (!half_wait<32>(&sm.s_full[sb], ph, wg, p.status, &sm.dead)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int k0 = first_key + t * BK;
-        if (k0 + BK > kvlim) {
-          // Values that no row of the tile may see: rows kvlim - k0 .. 127 of the stage.
-          const uint32_t vl = 2 * (tiles + t) + 1;
-          half_wait(&sm.ring_full[vl % STAGES], vl / STAGES, wg, p.status, nullptr);
-          const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
-          if (zrow >= kvlim - k0) {
-            uint4* const z = reinterpret_cast<uint4*>(smem + RING_OFF + (vl % STAGES) * TILE_BYTES + (zrow >> 3) * 2048 +
-                                                      zcol * 1024 + (zrow & 7) * 128);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) z[x] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-        }
         if (active) {
           // The maximum needs all 128 keys, in two loads of 64; the second one's stay in
           // registers, the first one's are read again for their exponentials, 32 keys at a time
@@ -1032,15 +1110,21 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       // ---- the item's output: O / l, or the partial
       l[0] = quad_sum(l[0]);
       l[1] = quad_sum(l[1]);
+      auto put_late = [&] {
+        const int first = pair ? wg * p.tq : 0, row = lane0 + lane / 4;
+        if (__builtin_expect(it.late, 0)) add_late(sm.late[slot], ocol, first + row / p.G, first + (row + 8) / p.G);
+      };
       const bool adds = it.added && it.part < 0;
       if (__builtin_expect(adds, 0)) {
         if (!half_wait(&sm.o_full[wg], outs, wg, p.status, &sm.dead)) break;
         tc_fence_after();
-        if (active)
+        if (active) {
+          put_late();
           for (int i = 1; i <= it.added; ++i)
             add_part(p.parts + (size_t)(2 * (blockIdx.x + i)) * PART_BYTES,
                      p.flags + (blockIdx.x + i) * SOFTMAX_WARPS + warp, p.call, p.status,
                      (pair ? wg * 128 : 0) + lane0 + lane / 4, valid, ocol, m, l);
+        }
       }
       float inv[2];
       uint16_t* dst[2];
@@ -1058,6 +1142,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       ++outs;
       tc_fence_after();
       if (active) {
+        if (!adds) put_late();
         if (it.part < 0) {
           auto store = [&](const uint32_t(&o)[16], int y) {  // 32 columns: four groups of eight
 #pragma unroll

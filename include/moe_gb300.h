@@ -473,10 +473,11 @@ moe_status_t moe_paged_append(const moe_paged_shape_t* shape, const void* qkv, c
  *        for two seconds at most, then MOE_ERR_TIMEOUT is set and outputs are unspecified;
  *        clear it before a captured call that timed out is replayed
  * Rows without keys (padding rows; all rows of a request with kv_len < n, as a denied one)
- * get out = 0 and lse = -inf.  What the pages hold past a request's keys is never used,
- * NaN and infinities included.  A NaN among a row's own scores makes the row NaN; a
- * non-finite value of the request may also reach the rows up to 127 positions before it.  row_start is non-decreasing within [0, T] and
- * kv_len at most max_pages * page_size, else MOE_ERR_DEVICE is set and the rows concerned
+ * get out = 0 and lse = -inf.  A row depends on the keys and values that it sees alone, NaN
+ * and infinities of later tokens and of what the pages hold past a request's keys included:
+ * they do not reach it.  A NaN among a row's own scores makes the row NaN; a NaN or infinity
+ * among the values that it sees makes that column so.  row_start is non-decreasing within
+ * [0, T] and kv_len at most max_pages * page_size, else MOE_ERR_DEVICE is set and the rows concerned
  * are unspecified, as are those of a request with a table entry in use outside [0, pages).
  * The sums run in an order that depends on the lengths alone: equal calls give equal bits. */
 size_t moe_paged_attention_workspace_size(const moe_paged_shape_t* shape);

@@ -723,3 +723,55 @@ def test_plan_in_place(R, max_pages, pad, which):
         s["new"] = np.where(np.cumsum(np.maximum(room, 0)) <= T, room, 0)
     assert denied or R < 700  # the pool runs short in the larger ones
     assert M.moe_device_status() == 0
+
+
+# (ctx, new, n_head, n_kv_head, page): work tiles of 256 tokens (no grouping) down to 16, whole and
+# cut, their first tokens at a key tile's beginning and inside one.
+LATE_VALUES = {
+    "no-grouping-prompt": ([0], [256], 2, 2, 16),
+    "no-grouping-odd": ([64, 5], [300, 1], 4, 4, 16),
+    "no-grouping-long": ([5000], [520], 1, 1, 64),
+    "groups-of-2": ([40], [200], 4, 2, 32),
+    "groups-of-3": ([100, 2], [70, 9], 6, 2, 64),
+    "groups-of-4": ([100, 700], [200, 1], 8, 2, 16),
+    "groups-of-4-prompt": ([0, 0], [129, 40], 8, 2, 128),
+    "groups-of-16": ([30], [40], 16, 1, 16),
+    "verification": ([9000, 300], [7, 5], 8, 2, 64),
+    "chunk-in-many-parts": ([20000], [64], 8, 2, 32),
+    "chunks-in-three-parts": ([6000, 5000], [700, 27], 4, 1, 128),
+}
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("name", LATE_VALUES)
+def test_attention_values_reach_no_earlier_row(name, value):
+    """NaN and infinities in the values of a request's new tokens: the rows from that position on
+    have them in that column, every other output has equal bits, and so has every lse."""
+    ctx, new, H, KV, page = LATE_VALUES[name]
+    a = _attn_inputs(np.random.default_rng(41), ctx, new, H, KV, page, pad=3)
+    ref_out, ref_lse = _attend(a)
+    n, G, inf = new[0], H // KV, float("inf")
+    put = [(0, 0, value), (1, 9, value), (n // 3, 63, value), (n // 2, 64, value), (n - 2, 100, value),
+           (n - 1, 127, value), (n // 3, 37, inf), (2 * n // 3, 37, -inf), (n // 4, 90, value), (n // 2, 90, value)]
+    b = dict(a, v=a["v"].clone())
+    want = ref_out.clone().reshape(-1, H, 128)
+    for i, col, x in put:
+        pos = ctx[0] + i
+        b["v"][int(a["table"][0][pos // page]), 0, pos % page, col] = x
+        want[i:n, :G, col] += x  # inf - inf gives NaN
+    out, lse = _attend(b, calls=2)
+    out = out.reshape(-1, H, 128)
+    assert torch.equal(lse, ref_lse)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    keep = ~torch.isnan(want)
+    assert torch.equal(out[keep].view(torch.int16), want[keep].view(torch.int16))
+    # A whole row of values.
+    b = dict(a, v=a["v"].clone())
+    pos = ctx[0] + n - 1
+    b["v"][int(a["table"][0][pos // page]), :, pos % page] = value
+    out, lse = _attend(b)
+    want = ref_out.clone()
+    want[n - 1] += value
+    assert torch.equal(lse, ref_lse) and torch.equal(out.isnan(), want.isnan())
+    keep = ~want.isnan()
+    assert torch.equal(out[keep].view(torch.int16), want[keep].view(torch.int16))
