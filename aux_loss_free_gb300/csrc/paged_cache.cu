@@ -224,7 +224,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanPara
   // The ended requests' pages, behind the free ones.
   for (int k = blockIdx.x * PLAN_THREADS + tid; k < returned && count + k < p.pages; k += gridDim.x * PLAN_THREADS) {
     const int r = find_range(s_back, p.R, k);
-    p.pool[ring(count + k)] = p.table[(long long)r * p.max_pages + (k - s_back[r])];
+    const int id = p.table[(long long)r * p.max_pages + (k - s_back[r])];
+    if (id < 0 || id >= p.pages) bad = true;
+    p.pool[ring(count + k)] = id;
   }
   if (bad) atomicOr(p.status, kDevCheck);
 }

@@ -441,8 +441,8 @@ typedef struct {
  * it are more than `count` (later requests that need no page are still served), or when it
  * does not fit: ctx_len outside [0, max_pages * page_size], more than max_pages pages, rows
  * past T.  A request that does not fit asks for no page; that, a pool state outside
- * [0, pages) x [0, pages] and a table entry in use that is no page set MOE_ERR_DEVICE in the
- * device status word.  The outputs depend on the inputs alone, so the call can be repeated on
+ * [0, pages) x [0, pages] and a table entry, in use or given back, that is no page set
+ * MOE_ERR_DEVICE in the device status word.  The outputs depend on the inputs alone, so the call can be repeated on
  * the same inputs; no input but block_table and pool overlaps an output, except that a step
  * can be taken in place: next_ctx == ctx_len and pool_state_out == pool_state_in (either or
  * both) replace the present lengths and pool state by the next ones, and a captured call then

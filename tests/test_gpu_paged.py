@@ -775,3 +775,22 @@ def test_attention_values_reach_no_earlier_row(name, value):
     assert torch.equal(lse, ref_lse) and torch.equal(out.isnan(), want.isnan())
     keep = ~want.isnan()
     assert torch.equal(out[keep].view(torch.int16), want[keep].view(torch.int16))
+
+
+@pytest.mark.parametrize("entry", [-1, "pages"])
+def test_plan_reports_a_returned_page_that_is_none(entry):
+    """An ended request's table holds no page where its context says that one is: reported in
+    the step that puts it back, not when another request is given it."""
+    s = _random_step(np.random.default_rng(17), 3, 16, 8, [-1, 1, -1], free=2)
+    s["ctx"] = np.array([40, 5, 17])
+    s["pages"] = 12
+    s["table"] = np.full((3, 8), -1)
+    s["table"][0, :3], s["table"][1, 0], s["table"][2, :2] = [1, 2, 3], 4, [5, 6]
+    s["pool"] = np.array([7, 8] + [-1] * 10)
+    s["state"] = [0, 2]
+    _check_plan(s, 16)
+    assert M.moe_device_status() == 0
+    s["table"][2, 1] = s["pages"] if entry == "pages" else entry
+    got = _run_plan(s, 16)
+    assert M.moe_device_status() == 6
+    assert got["slot_map"].tolist() == [4 * 16 + 5] and got["info"].tolist() == [1, 0, 5, 0]
