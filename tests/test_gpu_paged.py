@@ -794,3 +794,53 @@ def test_plan_reports_a_returned_page_that_is_none(entry):
     got = _run_plan(s, 16)
     assert M.moe_device_status() == 6
     assert got["slot_map"].tolist() == [4 * 16 + 5] and got["info"].tolist() == [1, 0, 5, 0]
+
+
+def _prepared(a, stream):
+    """A call on `a` in buffers of its own; returns it with its outputs."""
+    T = a["q"].shape[0]
+    shape = M.make_paged_shape(len(a["kv"]), T, a["H"], a["KV"], a["page"], a["pages"], a["table"].shape[1])
+    ws = torch.randint(0, 256, (M.moe_paged_attention_workspace_size(shape),), dtype=torch.uint8, device=DEV)
+    dev = [_i32(a["table"]), _i32(a["row_start"]), _i32(a["kv"])]
+    out = torch.empty(T, a["H"] * 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(T, a["H"], dtype=torch.float32, device=DEV)
+    return lambda: M.moe_paged_attention(shape, a["q"], a["k"], a["v"], *dev, out, lse, ws, stream=stream), out, lse
+
+
+# Pairs of calls: work tiles that are joined by the CTA of their first part, tiles in many parts,
+# decode steps.
+TWO_STREAMS = [(([3000, 100, 5000], [400, 700, 1], 8, 2, 16), ([9000, 10], [64, 1300], 8, 2, 32)),
+               (([0], [2048], 8, 2, 64), ([20000, 3], [5, 1], 4, 1, 128)),
+               (([600, 0], [900, 300], 2, 2, 64), ([500] * 40, [1] * 40, 8, 2, 16))]
+
+
+@pytest.mark.parametrize("pair", range(len(TWO_STREAMS)))
+def test_attention_on_two_streams_at_once(pair):
+    """Two calls with workspaces of their own, queued on two streams again and again without a
+    wait between them: the bits of the calls alone, and a clear status word.  Parts of a call wait
+    for other parts of it while the other call holds SMs."""
+    rng = np.random.default_rng(60 + pair)
+    ins = [_attn_inputs(rng, *c[:2], *c[2:], pad=2) for c in TWO_STREAMS[pair]]
+    alone = [_attend(a) for a in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    calls = [_prepared(a, s) for a, s in zip(ins, streams)]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for call, _, _ in calls:
+            call()
+    torch.cuda.synchronize()
+    for (_, out, lse), (ref, ref_lse) in zip(calls, alone):
+        assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(lse, ref_lse)
+    assert M.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_at_random_shapes(seed):
+    """Lengths, groups (powers of two and others), pages and padding drawn from the seed."""
+    rng = np.random.default_rng(1000 + seed)
+    KV, G = int(rng.choice([1, 2, 4])), int(rng.choice([1, 2, 3, 4, 5, 7, 8, 16]))
+    R, page = int(rng.integers(1, 9)), int(rng.choice([16, 32, 64, 128]))
+    ctx = [int(np.exp(rng.uniform(0, np.log(6000)))) - 1 for _ in range(R)]
+    new = [int(rng.choice([0, 1, 1, 5, rng.integers(1, 300), rng.integers(1, 1200)])) for _ in range(R)]
+    new[0] = max(new[0], 1)
+    _check_attention(_attn_inputs(rng, ctx, new, KV * G, KV, page, int(rng.choice([0, 1, 40]))), calls=2)
