@@ -151,20 +151,29 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_torch_c = None
+_current = None
+
+
+def _current_stream():
+    """How the current stream's handle is read: from PyTorch's own per-device word (0.3 us) where
+    this PyTorch has these two calls, which are not public; else from a Stream object, whose
+    making takes 3 us, as long as a launch."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
 
 def _stream(stream):
-    """The stream's handle; by default PyTorch's current stream of the current device.  Read
-    from PyTorch's own per-device word (0.3 us): building a Stream object for it takes 3 us, as
-    long as a launch."""
-    global _torch_c
+    """The stream's handle; by default PyTorch's current stream of the current device."""
+    global _current
     if stream is not None:
         return stream.cuda_stream
-    if _torch_c is None:
-        from torch import _C
-        _torch_c = _C
-    return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+    if _current is None:
+        _current = _current_stream()
+    return _current()
 
 
 def _check(name: str, code: int):

@@ -2,6 +2,7 @@
 the oracle's step plan and paged attention agree with hand-worked values and the dense
 oracle."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -178,3 +179,18 @@ def test_the_block_refuses_other_rows(step, name, which):
         block.forward(*((make(), good) if which == "x" else (good, make())))
     with pytest.raises(ValueError, match="CUDA device"):
         block.forward(good, good)
+
+
+@pytest.mark.parametrize("missing", [None, "_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_the_current_stream_without_pytorchs_own_calls(monkeypatch, missing):
+    """The calls that read the handle directly are not public: without one of them it comes from
+    the public Stream object."""
+    for name, value in (("_cuda_getCurrentRawStream", lambda d: 100 + d), ("_cuda_getDevice", lambda: 3)):
+        if name == missing:
+            monkeypatch.delattr(torch._C, name, raising=False)
+        else:
+            monkeypatch.setattr(torch._C, name, value, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=7))
+    monkeypatch.setattr(M._lib, "_current", None, raising=False)
+    assert M._lib._stream(None) == (7 if missing else 103)
+    assert M._lib._stream(types.SimpleNamespace(cuda_stream=9)) == 9
