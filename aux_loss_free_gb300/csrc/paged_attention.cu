@@ -161,7 +161,7 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 __device__ __forceinline__ Request load_request(const PagedParams& p, int r, bool report) {
   Request q;
   const int a = p.row_start[r], b = r < p.R ? p.row_start[r + 1] : p.T;
-  const bool rows_ok = a >= 0 && a <= b && b <= p.T;
+  const bool rows_ok = a >= 0 && a <= b && b <= p.T && (r > 0 || a == 0);
   const int kv = r < p.R ? p.kv_len[r] : 0;
   const bool kv_ok = kv <= (p.max_pages << p.page_shift);
   if (report && !(rows_ok && kv_ok)) atomicOr(p.status, kDevCheck);

@@ -476,9 +476,10 @@ moe_status_t moe_paged_append(const moe_paged_shape_t* shape, const void* qkv, c
  * get out = 0 and lse = -inf.  A row depends on the keys and values that it sees alone, NaN
  * and infinities of later tokens and of what the pages hold past a request's keys included:
  * they do not reach it.  A NaN among a row's own scores makes the row NaN; a NaN or infinity
- * among the values that it sees makes that column so.  row_start is non-decreasing within
- * [0, T] and kv_len at most max_pages * page_size, else MOE_ERR_DEVICE is set and the rows concerned
- * are unspecified, as are those of a request with a table entry in use outside [0, pages).
+ * among the values that it sees makes that column so.  row_start[0] is 0, row_start does not
+ * decrease within [0, T] and kv_len is at most max_pages * page_size, else MOE_ERR_DEVICE is set
+ * and the rows concerned are unspecified, as are those of a request with a table entry in use
+ * outside [0, pages).  out and lse overlap no input.
  * The sums run in an order that depends on the lengths alone: equal calls give equal bits. */
 size_t moe_paged_attention_workspace_size(const moe_paged_shape_t* shape);
 moe_status_t moe_paged_attention(const moe_paged_shape_t* shape, const void* q, const void* k_cache,

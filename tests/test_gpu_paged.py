@@ -844,3 +844,13 @@ def test_attention_at_random_shapes(seed):
     new = [int(rng.choice([0, 1, 1, 5, rng.integers(1, 300), rng.integers(1, 1200)])) for _ in range(R)]
     new[0] = max(new[0], 1)
     _check_attention(_attn_inputs(rng, ctx, new, KV * G, KV, page, int(rng.choice([0, 1, 40]))), calls=2)
+
+
+def test_attention_reports_rows_before_the_first_request():
+    """row_start[0] is 0: rows before it would belong to no request and stay unwritten."""
+    a = _attn_inputs(np.random.default_rng(18), [100, 40], [3, 3], 8, 2, 16)
+    ref, _ = _attend(a)
+    assert M.moe_device_status() == 0
+    out, _ = _attend(dict(a, row_start=np.array([1, 3, 6])))
+    assert M.moe_device_status() == 6
+    assert torch.equal(out[3:].view(torch.int16), ref[3:].view(torch.int16))
