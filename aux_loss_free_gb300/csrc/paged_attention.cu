@@ -522,7 +522,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (base & 1023u) {  // the swizzled tiles need it; the declaration asks for it
-    if (tid == 0) atomicOr(p.status, kDevCheck);
+    if (tid == 0) {
+      atomicOr(p.status, kDevCheck);
+      pdl_wait();
+      p.splits[blockIdx.x] = Split{0, 0, 0, -1};  // nothing for paged_combine_kernel to join
+    }
     return;
   }
 
