@@ -68,11 +68,6 @@ struct AttnParams {
   float scale_log2;  // log2(e) / sqrt(HD)
 };
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // One warp per token row: every query and key head of the row (u / sqrt(mean(u^2) +
 // eps) over the head's 128 values, rounded to bf16 in place); all of the row's loads are
 // issued before the first reduction.

@@ -372,11 +372,6 @@ __device__ __forceinline__ int tile_set(int tile, int shared_tiles, int total) {
   return shared_tiles > 0 && tile < shared_tiles ? 0 : 1;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // silu(a) = a / (1 + e^-a).  The fast division has no special-value slow path; for
 // very negative a the denominator overflows and the quotient is the correct 0.
 __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }

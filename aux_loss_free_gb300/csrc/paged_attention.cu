@@ -92,7 +92,7 @@ constexpr int THREADS = 576;
 constexpr int WARPS = THREADS / 32;
 constexpr int ITEMS = 4;                      // depth of the item ring
 constexpr int CTAS = 152;                     // one per SM
-constexpr int P_PARTS = 3;                     // hardware barriers 3 .. 8: P's three parts, each of the two halves
+constexpr int PART_BAR = 3;                    // hardware barriers 3 .. 8: P's three parts, each of the two halves
 constexpr uint32_t O_COL = 256;               // score buffers at 0 and 128, outputs at 256 and 384
 constexpr uint32_t TMEM_COLS = 512;
 constexpr unsigned FULL = 0xFFFFFFFFu;
@@ -293,11 +293,6 @@ __device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, 
   w = __shfl_sync(FULL, w, 0);
   __syncwarp();  // what lane 0 acquired is every lane's
   return w != 0;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // The same for the eight warps of a query half (hardware barrier 1 + wg): one lane of the first
@@ -830,13 +825,13 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             if (h == 0 && !(ok = warp_wait_all(full(val), val.phase, full(last), last.phase, full(last), last.phase,
                                                p.status)))
               break;
-            part_wait(P_PARTS + h);
+            part_wait(PART_BAR + h);
             tc_fence_after();
             value(h, h, val.stage, 4, 4, t == 0);
-            part_wait(P_PARTS + 2 + h);
+            part_wait(PART_BAR + 2 + h);
             tc_fence_after();
             value(h, h, val.stage, 0, 2, false);
-            part_wait(P_PARTS + 4 + h);
+            part_wait(PART_BAR + 4 + h);
             tc_fence_after();
             value(h, h, val.stage, 2, 2, false);
             if (more) {
@@ -1074,7 +1069,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           if (pair) {
             tmem_wait_st();
             tc_fence_before();
-            part_arrive(P_PARTS + wg);
+            part_arrive(PART_BAR + wg);
           }
           tmem_ld_quad4(scol + 32, vb);
           tmem_wait_quad4(va, vb);
@@ -1084,7 +1079,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           if (pair) {
             tmem_wait_st();
             tc_fence_before();
-            part_arrive(P_PARTS + 2 + wg);
+            part_arrive(PART_BAR + 2 + wg);
           }
           weights(vb, 1);
           l[0] += ls[0].x + ls[0].y;
@@ -1094,10 +1089,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         tc_fence_before();
         if (pair) {
           if (!active) {
-            part_arrive(P_PARTS + wg);
-            part_arrive(P_PARTS + 2 + wg);
+            part_arrive(PART_BAR + wg);
+            part_arrive(PART_BAR + 2 + wg);
           }
-          part_arrive(P_PARTS + 4 + wg);
+          part_arrive(PART_BAR + 4 + wg);
         } else {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[b]));

@@ -254,11 +254,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_advance_kernel(int32_t* ct
   }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 struct AppendParams {
   const uint16_t* qkv;
   const int32_t* slot_map;
