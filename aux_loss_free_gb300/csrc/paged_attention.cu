@@ -35,7 +35,8 @@
 //     product that overwrites a buffer needs no wait for the product that read P from it.  A
 //     pair's P comes in three parts (keys 64-127, 0-31, 32-63): the value product of a part runs
 //     while the next is computed, and only the last one's lies between the softmax and the next
-//     scores (one part: 138 us, two: 129, three: 127 for 2 x 2011 tokens over long contexts);
+//     scores (one part: 138 us, two: 129, three: 127 for 2 x 2011 tokens over long contexts, one after
+//     the other on one GPU);
 //   - warps 0-7 and 8-15, a warp per 16 rows: the online softmax in the log2 domain.  TMEM is
 //     read in the 16 x 256-bit shape, four lanes per row with 32 scores each, so that two
 //     warps per SM sub-partition share a half tile and the row maximum is two shuffles; O is
@@ -56,14 +57,15 @@
 // a half that has an item arrives at every one of them, whatever became of its own waits.
 //
 // Bounds and measurements (8 query heads on 2 key/value heads; time of a call among others).
-// One token for each of 64 requests with 1000 to 16000 keys: 549 MB of keys and values, 92.5 us,
-// 5.9 TB/s; between its first copy and its last output a CTA streams at 6.3 TB/s, the rest is the
-// start (6 us: two dependent loads, the first copies and each instruction's first fetch) and the
-// joins (5 us).  2 x 2011 tokens over 1000 to 14000 keys: 176 GFLOP, 127 us, 1.39 PFLOP/s: a half
-// tile's chain (3.1k cycles: 0.75k maximum, 1.0k weights, 1.3k from the last part of P over its
-// value product and the next scores back to the warps) is longer than both halves' products (2k),
-// and tensor memory has no columns for a third half.  Both limits are latency; neither memory nor
-// the pipe is saturated.
+// One token for each of 64 requests with 1000 to 16000 keys: 549 MB of keys and values, 93.6 to
+// 94.0 us, 5.9 TB/s; between its first copy and its last output a CTA streams at 6.3 TB/s, the
+// rest is the start (6 us: two dependent loads, the first copies and each instruction's first
+// fetch) and the joins (5 us).  2 x 2011 tokens over 1000 to 14000 keys: 176 GFLOP, 125 to 132 us
+// from GPU to GPU (most 130: 1.35 PFLOP/s, 72% of the measured bf16 peak): a half tile's chain
+// (3.1k cycles: 0.75k maximum, 1.0k weights, 1.3k from the last part of P over its value product
+// and the next scores back to the warps) is longer than both halves' products (2k), and tensor
+// memory has no columns for a third half.  Both limits are latency; neither memory nor the pipe
+// is saturated.
 #include <cuda_bf16.h>
 #include <math.h>
 

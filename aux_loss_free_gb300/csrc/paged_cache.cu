@@ -15,12 +15,13 @@
 // writes the table entry: no separate pass over the table.  The call moves a few bytes per
 // token; it is bound by the launch and the chain load - sums - search - pool load - store: 3.2
 // to 3.7 us a launch for a step of up to 8 requests, 6.6 us for 1021 requests and 8072 rows (with
-// the ctypes call around it 4.9 and 7.1 us; the first form, sums in one serial pass: 9.9 and 11.2).
+// the ctypes call around it 4.9 and 7.2 us; the first form, sums in one serial pass: 9.9 and 11.2).
+// In place a step of one CTA costs the same, a larger one a second small launch (paged_advance_kernel).
 //
 // paged_append_kernel: one warp per token row; q and k heads normalised in fp32, q to its
 // row, k and v to their page.  A copy with a reduction, bound by memory traffic: 8192 rows of
-// 8 + 2 + 2 heads (50 MB) in 8.4 us, 7.0 us back to back in a captured graph where the writes
-// stay in L2; 64 rows in 2.8 us.
+// 8 + 2 + 2 heads (50 MB) in 8.4 us among other calls, 7.0 us back to back in a captured graph
+// where the writes stay in L2, 12.2 us under ncu with cold caches; 64 rows in 2.8 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>

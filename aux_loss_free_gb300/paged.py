@@ -37,7 +37,10 @@ class PagedStep:
     length is 0 then), grows with every step, and gives its pages back in the step that
     passes -1 for it; its row can start another request from the next step on.  `info`
     (rows in use, pages taken, pages returned, requests denied) tells what a step did; a
-    denied request keeps its context and can be tried again."""
+    denied request keeps its context and can be tried again.
+
+    A plan replaces the lengths that the last one left, on the stream that it is given: plans and
+    the calls that use their tables belong to one stream, or to streams that wait for each other."""
 
     def __init__(self, requests: int, pages: int, page_size: int, max_pages: int, max_tokens: int, device="cuda"):
         dev = torch.device(device)

@@ -490,7 +490,7 @@ moe_status_t moe_paged_attention(const moe_paged_shape_t* shape, const void* q, 
 /* The whole block of moe_attention_fwd over a paged cache: projections, moe_paged_append,
  * moe_paged_attention, output projection and (if residual) x added.  x and out [T][d] bf16,
  * w_qkv and w_o as for moe_attention_fwd, d % 64 == 0 (64 <= d <= 8192); q_stride is
- * not read.  The tables are one moe_paged_plan's; slot_map counts for rows before
+ * held to the same limits as for the other calls and has no effect here.  The tables are one moe_paged_plan's; slot_map counts for rows before
  * row_start[requests] alone, the others write no cache whatever it holds there. */
 size_t moe_attention_paged_workspace_size(const moe_paged_shape_t* shape, int32_t d);
 moe_status_t moe_attention_paged_fwd(const moe_paged_shape_t* shape, int32_t d, const void* x, const void* w_qkv,
