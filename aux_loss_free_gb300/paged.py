@@ -47,10 +47,11 @@ class PagedStep:
     With `sharing`, rows can branch off others, be cut back (fork) and be moved together (compact) between
     two plans; requests that end give back the pages that no other row holds, and `pages_info`
     (copies, pages given back, rows cut short, pages in use) tells what the last of these calls did.
-    With `window` (and `sinks`) too, every plan also gives back the pages that no later token sees: every
-    layer's attention then has a window of at most this one and at most these sinks, and a row can be cut
+    With `window` (and `sinks`) too, every plan also gives back the pages that no later token sees, but for one
+    page of a row at most: every layer's attention then has a window of at most this one and at most these sinks, and a row can be cut
     back or branched off no further back than it stood when it was last planned or forked (what its next token
-    should see is gone then: the attention reports MOE_ERR_DEVICE)."""
+    should see is gone then: the attention reports MOE_ERR_DEVICE).  A row that fork cuts short, because
+    the pool has no page for its copy, goes on from the whole pages that it kept."""
 
     def __init__(self, requests: int, pages: int, page_size: int, max_pages: int, max_tokens: int, device="cuda",
                  sharing: bool = False, window: int = 0, sinks: int = 0):
@@ -60,6 +61,9 @@ class PagedStep:
             raise ValueError("pages are given back behind a window with sharing=True alone")
         dev = torch.device(device)
         self.sharing, self.window, self.sinks = sharing, window, sinks
+        # A row that is cut short later loses up to page_size - 1 tokens, and its window moves back by as
+        # many: what it sees then is kept from the start, at most one page of a row.
+        self._kept = min(window + page_size - 1, (1 << 31) - 1) if window else 0
         self.requests, self.pages, self.page_size, self.max_pages = requests, pages, page_size, max_pages
         self.max_tokens = max_tokens
         self.tokens = 0  # rows of the step that was planned (or captured) last
@@ -105,7 +109,7 @@ class PagedStep:
         _check_cuda(ctx.device)
         shape = self.shape(tokens)
         if self.sharing:
-            L.moe_paged_release(shape, new_len, self.window, self.sinks, ctx, self.block_table, self.pool, state,
+            L.moe_paged_release(shape, new_len, self._kept, self.sinks, ctx, self.block_table, self.pool, state,
                                 self.pages_info, self._workspace, stream=stream)
         L.moe_paged_plan(shape, ctx, new_len, self.block_table, self.pool, state, state, self.row_start,
                          self.slot_map, self.kv_len, ctx, self.info, stream=stream)
@@ -137,7 +141,7 @@ class PagedStep:
             if t is not None:
                 _check(name, t, torch.int32, (self.requests,), ctx.device)
         self._between_steps()
-        L.moe_paged_fork(self.shape(1), parent, keep, self.window, self.sinks, ctx, self.block_table, self.block_table,
+        L.moe_paged_fork(self.shape(1), parent, keep, self._kept, self.sinks, ctx, self.block_table, self.block_table,
                          self.pool, state, state, ctx, self._copies, self.pages_info, self._workspace, stream=stream)
         self._copy(stream)
         return self

@@ -590,7 +590,10 @@ moe_status_t moe_attention_paged_window_fwd(const moe_paged_shape_t* shape, int3
  *   keep     [R] tokens that it takes over, at least 0 and at most ctx_len[parent[r]] (what is out of
  *            these limits is put to the nearest).  NULL = all
  *   window, sinks: with window > 0, pages that no later token sees (every key j of them has
- *            j >= sinks and j <= length - window) are given up too
+ *            j >= sinks and j <= length - window, length the tokens that the row takes over) are given up too.
+ *            Length is counted before a row is cut short (below): its window then reaches back by up to
+ *            page_size - 1 tokens more.  A caller whose pool can run short gives window + page_size - 1, for the
+ *            attention's window, in every fork and release, and a row that is cut short finds all that it sees
  *   ctx_len  [R] lengths before, next_ctx [R] after; may be the same
  *   table_in, table_out [R][max_pages]: before and after; the same, or not overlapping.  A row's entries
  *            in use are written, the others of table_out are left as they are
@@ -602,7 +605,7 @@ moe_status_t moe_attention_paged_window_fwd(const moe_paged_shape_t* shape, int3
  *            in row order.  The lowest row keeps the page itself if no row holds more of it
  *   info     [4]: copies, pages given back, rows cut short, pages in use afterwards
  * When the pool has no page left for a copy, that row and the later ones that want one are cut
- * short: their length is rounded down to whole pages.
+ * short: their length is rounded down to whole pages (behind a window see above).
  * moe_paged_release: the same with parent[r] = -1 where new_len[r] < 0, else r, in place; no row
  * is cut or copied, a page that several rows hold is counted and left to the others.  Called in front of
  * moe_paged_plan with the same new_len, it ends requests that share pages: the plan then finds their

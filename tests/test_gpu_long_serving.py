@@ -173,3 +173,41 @@ def test_serving_behind_a_window(graph):
     assert most > 24
     free = _serve(script, layers, step, graph)
     assert free[-1] == 24
+
+
+def test_rows_cut_short_behind_a_window_serve_on():
+    """A search behind a window in a full pool: branches without a page for their copy go on from whole pages, and their
+    next tokens see all that they should, the 40 keys behind them reaching into the first page."""
+    step = PagedStep(requests=5, pages=7, page_size=16, max_pages=10, max_tokens=112, sharing=True, window=40)
+    layers = [Layer(step, 5, dict(), 40, 0), Layer(step, 6, None, 17, 0)]
+    rng = np.random.default_rng(12)
+    x, h, y = (torch.zeros(112, D, dtype=torch.bfloat16, device=DEV) for _ in range(3))
+
+    def run(lens):
+        x.copy_(torch.tensor(rng.standard_normal((112, D)), dtype=torch.float32).to(DEV).to(torch.bfloat16))
+        step.plan(_i32(lens), 112)
+        layers[0].block.forward(x, h)
+        layers[1].block.forward(h, y)
+        torch.cuda.synchronize()
+        assert M.moe_device_status() == 0 and step.info.tolist()[3] == 0
+        for layer, src, out in ((layers[0], x, h), (layers[1], h, y)):
+            src, out, at = bf16_to_np(src), bf16_to_np(out), 0
+            for r, v in enumerate(lens):
+                layer.rows[r] = np.concatenate([layer.rows[r], src[at:at + v]]) if v >= 0 else np.zeros((0, D))
+                if v > 0:
+                    assert_close_bf16(out[at:at + v], layer.want(r, v), f"{lens}, row {r}")
+                    at += v
+
+    run([59, 0, 0, 0, 48])
+    run([1, 0, 0, 0, 0])
+    assert step.free_pages.item() == 0
+    step.fork(_i32([0, 0, 0, 0, 4]))
+    torch.cuda.synchronize()
+    assert step.ctx_len.tolist() == [60, 48, 48, 48, 48] and step.pages_info.tolist() == [0, 0, 3, 7]
+    for layer in layers:
+        layer.rows[1:4] = [layer.rows[0][:48]] * 3
+    run([1, 1, 5, 9, -1])
+    run([3, 1, 1, 1, 0])
+    run([0, 14, 10, 6, 0])
+    run([-1, -1, -1, -1, 0])
+    assert step.free_pages.item() == 7

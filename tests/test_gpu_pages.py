@@ -422,3 +422,36 @@ def test_calls_on_two_streams_at_once():
             was[dst, :, :t] = was[src, :, :t]
         assert torch.equal(cache.view(torch.int16), was.view(torch.int16))
     assert M.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("free", [0, 1, 2])
+@pytest.mark.parametrize("page,window,sinks", [(16, 24, 0), (16, 1, 0), (16, 17, 33), (64, 40, 4), (128, 300, 0)])
+def test_rows_cut_short_behind_a_window_find_what_they_see(page, window, sinks, free, in_place):
+    """Releases and forks that are given window + page_size - 1 for a window: in every row, cut short or not, the page of
+    every key that its next token sees is the parent's, or the copy of the parent's."""
+    cut = 0
+    for seed in range(4):
+        rng = np.random.default_rng(100 * seed + page + window)
+        R, width = 20, 12
+        s = _state(rng, R, page, width, free=free, share=0.0)
+        s["ctx"][:12] = 0  # rows that will branch off the others
+        new = np.where(rng.random(R) < 0.1, -1, 1)
+        kept = window + page - 1
+        ref = _check_release(s, new, kept, sinks)
+        s.update(ctx=ref["next_ctx"].astype(np.int64), table=ref["block_table"], pool=ref["pool"],
+                 state=[int(ref["pool_state"][0]), free])  # what came back is somebody else's
+        parent = np.r_[rng.integers(12, R, 12), np.arange(12, R)]
+        got = _run_fork(s, parent, None, kept, sinks, in_place=in_place)
+        copied = {int(d): int(a) for a, d, _, _ in got["copies"][:got["info"][0]]}
+        for r, q in enumerate(parent):
+            length, had = int(got["next_ctx"][r]), int(s["ctx"][q])
+            assert length == had or length == had // page * page
+            cut += length < had
+            keys = np.arange(length)
+            for j in np.unique(keys[(keys > length - window) | (keys < sinks)] // page):
+                id = int(got["block_table"][r, j])
+                assert 0 <= id < s["pages"], f"row {r}, {length} tokens: page {j} is {id}"
+                if id != s["table"][q, j]:
+                    assert copied[id] == s["table"][q, j] and (j + 1) * page > length
+    assert cut > 0 and M.moe_device_status() == 0

@@ -172,3 +172,91 @@ def test_a_step_without_sharing_does_not_keep_a_layers_caches(step):
     del layer
     gc.collect()
     assert [c() for c in caches] == [None, None]
+
+
+# --------------------------------------------------------- rows cut short behind a window
+
+def _put(tensor, values):
+    tensor.view(-1)[:np.asarray(values).size] = torch.as_tensor(np.asarray(values), dtype=torch.int32).view(-1)
+
+
+def _oracle_calls(monkeypatch):
+    """The step's calls answered by the oracles, on host tensors."""
+    n = lambda *ts: [None if t is None else t.numpy().copy() for t in ts]  # noqa: E731
+
+    def fork(shape, parent, keep, window, sinks, ctx, table, table_out, pool, state, state_out, next_ctx, copies, info,
+             workspace, stream=None):
+        got = P.fork(*n(parent, keep, ctx, table, pool, state), shape.pages, shape.page_size, window, sinks)
+        for t, k in ((table_out, "block_table"), (pool, "pool"), (next_ctx, "next_ctx"), (state_out, "pool_state"),
+                     (copies, "copies"), (info, "info")):
+            _put(t, got[k])
+
+    def release(shape, new_len, window, sinks, ctx, table, pool, state, info, workspace, stream=None):
+        got = P.release(*n(new_len, ctx, table, pool, state), shape.pages, shape.page_size, window, sinks)
+        for t, k in ((table, "block_table"), (pool, "pool"), (ctx, "next_ctx"), (state, "pool_state"), (info, "info")):
+            _put(t, got[k])
+
+    def plan(shape, ctx, new_len, table, pool, state, state_out, row_start, slot_map, kv_len, next_ctx, info, stream=None):
+        got = P.step_plan(*n(ctx, new_len, table, pool, state), shape.tokens, shape.pages, shape.page_size)
+        for t, k in ((table, "block_table"), (pool, "pool"), (next_ctx, "next_ctx"), (state_out, "pool_state"),
+                     (info, "info")):
+            _put(t, got[k])
+
+    for name, call in (("fork", fork), ("release", release), ("plan", plan)):
+        monkeypatch.setattr(paged.L, f"moe_paged_{name}", call)
+    monkeypatch.setattr(paged, "_check_cuda", lambda device: None)
+
+
+def _nothing_is_missing(st, window, sinks):
+    """Every key that a row's next token sees is in a page of its own table, which is not free."""
+    head, count = st._state.tolist()
+    free = {int(st.pool[(head + i) % st.pages]) for i in range(count)}
+    assert len(free) == count
+    for r, length in enumerate(st.ctx_len.tolist()):
+        for key in range(length):
+            if length - key < window or key < sinks:
+                page = int(st.block_table[r, key // st.page_size])
+                assert 0 <= page < st.pages and page not in free, f"row {r} of {length} tokens: key {key} in page {page}"
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_rows_cut_short_behind_a_window_keep_what_their_next_token_sees(lib, monkeypatch, seed):
+    """A search of eight rows behind a window in a pool that runs short, within what PagedStep allows: a row is cut
+    back no further than it stood when it was last planned or forked."""
+    _oracle_calls(monkeypatch)
+    rng = np.random.default_rng(4200 + seed)
+    R, page, cut = 8, 16, 0
+    window, sinks = int(rng.choice([2, 9, 16, 17, 24, 40, 70])), int(rng.choice([0, 4, 20]))
+    st = paged.PagedStep(requests=R, pages=-(-(window + sinks) // page) + int(rng.integers(5, 9)), page_size=page,
+                         max_pages=60, max_tokens=400, device="cpu", sharing=True, window=window, sinks=sinks)
+    stood = np.zeros(R, int)
+    for turn in range(90):
+        ctx = st.ctx_len.numpy().copy()
+        if turn % 3:  # a row that is empty stays so, all of them but the first
+            new = np.where(ctx > 0, rng.choice([0, 1, 2, 5], R), 0)
+            new[0] = new[0] if ctx[0] else 20
+            new[ctx > 850] = -1
+            st.plan(torch.tensor(new, dtype=torch.int32), 400)
+            stood = np.where(new < 0, 0, ctx)
+        else:
+            live = np.flatnonzero(ctx > 0) if ctx.any() else np.array([0])
+            parent = np.where(rng.random(R) < 0.6, rng.choice(live, R), np.arange(R))
+            back = np.where(rng.random(R) < 0.3, rng.integers(0, ctx - stood + 1), 0)
+            st.fork(torch.tensor(parent, dtype=torch.int32), torch.tensor((ctx - back)[parent], dtype=torch.int32))
+            cut += int(st.pages_info[2])
+            stood = st.ctx_len.numpy().copy()
+        _nothing_is_missing(st, window, sinks)
+    assert cut > 0
+
+
+def test_a_window_near_the_largest_is_kept(lib, monkeypatch):
+    seen = []
+    monkeypatch.setattr(paged, "_check_cuda", lambda device: None)
+    monkeypatch.setattr(paged.L, "moe_paged_release", lambda shape, new, window, *_, **__: seen.append(window))
+    monkeypatch.setattr(paged.L, "moe_paged_plan", lambda *_, **__: None)
+    monkeypatch.setattr(paged.L, "moe_paged_fork", lambda shape, parent, keep, window, *_, **__: seen.append(window))
+    for window in (0, 1, (1 << 31) - 1):
+        st = paged.PagedStep(requests=2, pages=4, page_size=16, max_pages=2, max_tokens=8, device="cpu", sharing=True,
+                             window=window)
+        st.plan(torch.zeros(2, dtype=torch.int32), 8).fork()
+    assert seen == [0, 0, 16, 16, (1 << 31) - 1, (1 << 31) - 1]
