@@ -455,3 +455,25 @@ def test_rows_cut_short_behind_a_window_find_what_they_see(page, window, sinks, 
                 if id != s["table"][q, j]:
                     assert copied[id] == s["table"][q, j] and (j + 1) * page > length
     assert cut > 0 and M.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("free", [0, 1, 2, 7, 30])
+def test_as_many_rows_are_cut_short_as_copies_find_no_page(free):
+    """Forty rows go on, two from each of twenty that stay and end inside a page of their own; nothing comes back."""
+    for seed in range(4):
+        rng = np.random.default_rng(900 + seed)
+        ctx = np.r_[np.zeros(40, int), rng.integers(0, 6, 20) * 16 + rng.integers(1, 16, 20)]
+        held = -(-ctx // 16)
+        used = int(held.sum())
+        table = np.full((60, 6), -1)
+        ids = rng.permutation(used + free)
+        for r in range(60):
+            table[r, :held[r]] = ids[held[:r].sum():held[:r + 1].sum()]
+        pool = np.full(used + free, -7)
+        pool[:free] = ids[used:]
+        s = dict(ctx=ctx, table=table, pool=pool, state=[0, free], pages=used + free, page=16)
+        got = _run_fork(s, np.r_[40 + np.arange(40) % 20, 40 + np.arange(20)], None)
+        # Of three rows that end in a page the lowest keeps it: 40 copies are wanted.
+        assert got["info"][:3].tolist() == [free, 0, 40 - free]
+        assert (got["next_ctx"] < np.r_[ctx[40:], ctx[40:], ctx[40:]]).sum() == 40 - free
+    assert M.moe_device_status() == 0
