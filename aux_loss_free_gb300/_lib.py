@@ -203,6 +203,13 @@ def _check(name: str, code: int):
         raise MoEError(name, code)
 
 
+def _check_int32(**numbers: int):
+    """Numbers for an int32_t: of larger ones ctypes would pass the lower 32 bits."""
+    for name, v in numbers.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} {v} does not fit 32 bits")
+
+
 def make_shape(T, d, E, f, F, k, renorm=True, x_dtype=MOE_X_BF16, w_format=MOE_W_BF16) -> MoEShape:
     return MoEShape(T, d, E, f, F, k, int(bool(renorm)), x_dtype, w_format)
 
@@ -468,6 +475,7 @@ def moe_paged_append_rope(shape, rope, qkv, slot_map, row_start, kv_len, q, k_ca
 
 def moe_paged_window_attention(shape, window, sinks, q, k_cache, v_cache, block_table, row_start, kv_len, out, lse,
                                workspace, stream=None):
+    _check_int32(window=window, sinks=sinks)
     _check("moe_paged_window_attention", load_library().moe_paged_window_attention(
         ctypes.byref(shape), window, sinks, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(row_start),
         _ptr(kv_len), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -476,6 +484,7 @@ def moe_paged_window_attention(shape, window, sinks, q, k_cache, v_cache, block_
 
 def moe_attention_paged_window_fwd(shape, d, rope, window, sinks, x, w_qkv, w_o, residual, k_cache, v_cache,
                                    block_table, row_start, slot_map, kv_len, out, workspace, stream=None):
+    _check_int32(window=window, sinks=sinks)
     _check("moe_attention_paged_window_fwd", load_library().moe_attention_paged_window_fwd(
         ctypes.byref(shape), d, _ref(rope), window, sinks, _ptr(x), _ptr(w_qkv), _ptr(w_o), int(residual),
         _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(row_start), _ptr(slot_map), _ptr(kv_len), _ptr(out),
@@ -488,6 +497,7 @@ def moe_paged_pages_workspace_size(shape) -> int:
 
 def moe_paged_fork(shape, parent, keep, window, sinks, ctx_len, table_in, table_out, pool, pool_state_in,
                    pool_state_out, next_ctx, copies, info, workspace, stream=None):
+    _check_int32(window=window, sinks=sinks)
     _check("moe_paged_fork", load_library().moe_paged_fork(
         ctypes.byref(shape), _ptr(parent), _ptr(keep), window, sinks, _ptr(ctx_len), _ptr(table_in), _ptr(table_out),
         _ptr(pool), _ptr(pool_state_in), _ptr(pool_state_out), _ptr(next_ctx), _ptr(copies), _ptr(info),
@@ -496,6 +506,7 @@ def moe_paged_fork(shape, parent, keep, window, sinks, ctx_len, table_in, table_
 
 def moe_paged_release(shape, new_len, window, sinks, ctx_len, block_table, pool, pool_state, info, workspace,
                       stream=None):
+    _check_int32(window=window, sinks=sinks)
     _check("moe_paged_release", load_library().moe_paged_release(
         ctypes.byref(shape), _ptr(new_len), window, sinks, _ptr(ctx_len), _ptr(block_table), _ptr(pool),
         _ptr(pool_state), _ptr(info), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))

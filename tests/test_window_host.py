@@ -1,6 +1,7 @@
 """Paged attention with a window refuses what it cannot serve, before any launch (no GPU), and the oracle
 agrees with hand-worked values."""
 import ctypes
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -72,3 +73,18 @@ def test_window_oracle():
     whole = P.paged_attention(*args)
     np.testing.assert_array_equal(P.paged_attention(*args, window=44)["out"], whole["out"])
     np.testing.assert_array_equal(P.paged_attention(*args, window=1, sinks=44)["out"], whole["out"])
+
+
+@pytest.mark.parametrize("window,sinks", [(1 << 32, 0), ((1 << 32) + 5, 0), (1 << 31, 0), (9, 1 << 32), (-(1 << 32), 0)])
+def test_the_calls_refuse_windows_beyond_32_bits(lib, window, sinks):
+    """They would arrive as other numbers: 2^32 as no window at all."""
+    shape, none, on = M.make_paged_shape(**GOOD), torch.empty(0, dtype=torch.uint8), SimpleNamespace(cuda_stream=None)
+    for call in (lambda w, s: M.moe_paged_window_attention(shape, w, s, *[None] * 8, none, stream=on),
+                 lambda w, s: M.moe_attention_paged_window_fwd(shape, 1024, None, w, s, None, None, None, True,
+                                                               *[None] * 7, none, stream=on),
+                 lambda w, s: M.moe_paged_fork(shape, None, None, w, s, *[None] * 9, none, stream=on),
+                 lambda w, s: M.moe_paged_release(shape, None, w, s, *[None] * 5, none, stream=on)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call(window, sinks)
+        with pytest.raises(M.MoEError):  # these reach the library, which has no addresses
+            call((1 << 31) - 1, (1 << 31) - 1)
