@@ -440,6 +440,7 @@ def make_rope(rotary_dim=128, interleaved=False, base=10000.0, factor=1.0, train
               fast_turns=32.0, magnitude=1.0) -> MoERope:
     """A rotation for the calls below (moe_rope_init): frequencies base^(-2 i / rotary_dim), divided by
     `factor`, or with trained_len > 0 only as far as a pair is slow over that many tokens."""
+    _check_int32(rotary_dim=rotary_dim, trained_len=trained_len)
     rope = MoERope()
     _check("moe_rope_init", load_library().moe_rope_init(
         ctypes.byref(rope), rotary_dim, MOE_ROPE_INTERLEAVED if interleaved else MOE_ROPE_HALVES, base, factor,

@@ -155,3 +155,11 @@ def test_gradient_oracle_against_differences(interleaved, rot):
         e[r, c] = h
         diff = np.sum(dy * (R.norm_rope(u + e, *args) - R.norm_rope(u - e, *args))) / (2 * h)
         assert abs(diff - got[r, c]) <= 1e-7 * (1 + abs(got[r, c]))
+
+
+@pytest.mark.parametrize("kw", [dict(rotary_dim=(1 << 32) + 64), dict(trained_len=1 << 32), dict(trained_len=1 << 31)])
+def test_sizes_beyond_32_bits_are_refused(lib, kw):
+    """They would arrive as other numbers: a trained length of 2^32 as none."""
+    with pytest.raises(ValueError, match="32 bits"):
+        M.make_rope(factor=8.0, **kw)
+    M.make_rope(factor=8.0, trained_len=(1 << 31) - 1)
