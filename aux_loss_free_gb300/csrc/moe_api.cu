@@ -1266,7 +1266,7 @@ moe_status_t check_attn(const moe_attn_shape_t* s) {
   if (!s) return MOE_ERR_INVALID_ARG;
   if (s->batch < 1 || s->seq < 1 || s->d < 1 || s->n_head < 1 || s->n_kv_head < 1 || !(s->eps > 0.f))
     return MOE_ERR_INVALID_ARG;
-  if (s->head_dim != kAttnHeadDim || s->n_head % s->n_kv_head || s->n_head * kAttnHeadDim > 8192 ||
+  if (s->head_dim != kAttnHeadDim || s->n_head % s->n_kv_head || s->n_head > 8192 / kAttnHeadDim ||
       s->d % 64 || s->d > 8192 || (long long)s->batch * s->seq > (1LL << 24))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

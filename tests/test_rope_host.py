@@ -163,3 +163,15 @@ def test_sizes_beyond_32_bits_are_refused(lib, kw):
     with pytest.raises(ValueError, match="32 bits"):
         M.make_rope(factor=8.0, **kw)
     M.make_rope(factor=8.0, trained_len=(1 << 31) - 1)
+
+
+@pytest.mark.parametrize("n_head", [65, 1 << 24, 1 << 25, (1 << 25) + 8, (1 << 31) - 8])
+def test_more_heads_than_the_block_has_are_refused(lib, n_head):
+    """Values of a row past 8192, counted without a product that passes 32 bits."""
+    p, s = ctypes.c_void_p(16), ctypes.byref(M.make_attn_shape(1, 20, 1024, n_head, n_head // 4 if n_head % 4 == 0 else 1))
+    assert lib.moe_attention_workspace_size(s) == 0
+    assert lib.moe_attention_core(s, p, p, None) == 2
+    assert lib.moe_attention_fwd(s, p, p, p, 1, p, p, 1 << 30, None) == 2
+    assert lib.moe_qk_norm_rope(s, None, None, p, p, None) == 2
+    assert lib.moe_qk_norm_rope_bwd(s, None, None, p, p, p, None) == 2
+    assert lib.moe_attention_rope_fwd(s, None, None, p, p, p, 1, p, p, 1 << 30, None) == 2
