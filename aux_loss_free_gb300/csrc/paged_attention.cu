@@ -1078,7 +1078,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     const uint32_t tl = tmem + ((uint32_t)lane0 << 16);
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     uint32_t tiles = 0, pairs = 0, even = 0, odd = 0, outs = 0;  // even, odd: a single item's key tiles
-    bool ok = true;
+    bool ok = true, idle = false;  // idle: the second half without work in the item before
     for (uint32_t items = 0; ok; ++items) {
       const int slot = items % ITEMS;
       if (!half_wait(&sm.item_full[slot], items / ITEMS, wg, p.status, &sm.dead)) break;
@@ -1090,6 +1090,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[slot]));
         if (nt == 0) break;
         tiles += nt;
+        idle = true;
         continue;
       }
       const int kvlim = it.kvlim, first_key = it.j0 * BK;
@@ -1119,7 +1120,13 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         const bool low_edge = WIN && k0 < all_low && k0 + BK > p.sinks;
         if (k0 + BK > all_see || low_edge) {
           // Values that some row of the tile does not see: rows all_see - k0 .. 127 of the stage, no
-          // row from kvlim - k0 on.  While the tile's scores are computed.
+          // row from kvlim - k0 on.  While the tile's scores are computed; a half that has sat out single
+          // items waits for the scores first.  It may be ahead of the key tile two tiles back, whose copy into the
+          // same stage may still be landing: to a parity that looks as if this tile's had.
+          if (idle && !half_wait<32>(&sm.s_full[sb], ph, wg, p.status, &sm.dead)) {
+            ok = false;
+            break;
+          }
           const uint32_t vl = 2 * (tiles + t) + 1;
           half_wait(&sm.ring_full[vl % STAGES], vl / STAGES, wg, p.status, nullptr);
           const int zrow = tid & 127, zcol = (tid >> 7) & 1;  // one row's 128 bytes per thread of the eight warps
@@ -1149,6 +1156,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           ok = false;
           break;
         }
+        idle = false;
         tc_fence_after();
         if (active) {
           // The maximum needs all 128 keys, in two loads of 64; the second one's stay in

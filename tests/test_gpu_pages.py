@@ -477,3 +477,25 @@ def test_as_many_rows_are_cut_short_as_copies_find_no_page(free):
         assert got["info"][:3].tolist() == [free, 0, 40 - free]
         assert (got["next_ctx"] < np.r_[ctx[40:], ctx[40:], ctx[40:]]).sum() == 40 - free
     assert M.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("pages", [1 << 17, (1 << 17) + 1, 1 << 18, (1 << 18) + 1])
+def test_caches_around_the_most_pages_with_marks_in_shared_memory(pages):
+    """A block's share of the pages doubles behind 2^17; behind 2^18 the marks are in the workspace.  Pages of both ends
+    of the cache are in use."""
+    rng = np.random.default_rng(pages % 1000)
+    s = _state(rng, 100, 16, 40, free=0)
+    used = s["pages"]
+    spread = np.sort(rng.choice(pages - 2, used - 2, replace=False)) + 1
+    ids = rng.permutation(np.r_[0, spread, pages - 1])
+    inside = np.arange(40)[None] < -(-s["ctx"] // 16)[:, None]
+    s["table"] = np.where(inside & (s["table"] >= 0), ids[np.clip(s["table"], 0, used - 1)], s["table"])
+    free = np.setdiff1d(np.arange(pages), ids)
+    pool = np.full(pages, -7)
+    pool[(pages - 5 + np.arange(len(free))) % pages] = rng.permutation(free)
+    s.update(pages=pages, pool=pool, state=[pages - 5, len(free)])
+    for in_place in (True, False):
+        _check_fork(s, *_branches(rng, s, "few"), in_place=in_place)
+        assert _check_compact(s, in_place)["info"][3] == used
+    _check_release(s, np.where(rng.random(100) < 0.3, -1, 1), 100, 4)
+    assert M.moe_device_status() == 0
