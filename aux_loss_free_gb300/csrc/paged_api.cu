@@ -171,7 +171,8 @@ moe_status_t moe_attention_paged_window_fwd(const moe_paged_shape_t* shape, int3
   cudaError_t e = launch_grouped_gemm(off, nullptr, 1, proj, none, 0, s, &bad);
   if (bad) return MOE_ERR_UNSUPPORTED;
   // The query heads are normalised where the projection left them.  Rows past the plan's write
-  // no cache: a slot map that a larger step has filled holds live slots there.
+  // no cache: a slot map that a larger step has filled holds live slots there.  Without a rotation the kernel
+  // without one is the faster (rope.cu has the figures).
   if (e == cudaSuccess)
     e = rope ? launch_paged_append_rope(*shape, rope, qkv, slot_map, row_start, kv_len, qkv, C,
                                         static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache), s)

@@ -80,8 +80,8 @@
 // is 6 us, the last tile's softmax, the output and the second launch 3 us); four 2048-token prompts with a
 // window of 512 33 to 35 us (15 GFLOP): a CTA has one or two work tiles of five key tiles, two or three of them
 // at an edge, whose masks and search add 0.7k to 1.7k cycles to a tile's 1.7k of softmax.  Skipping what no row
-// of a warp sees (no exponentials for groups of 32 hidden keys) was slower by 12%: the branches part the
-// exponentials from the loads that run beside them.
+// of a warp sees (no exponentials for groups of 32 hidden keys) was slower, 37.1 us for 32.5 (back to back in a
+// graph): the branches part the exponentials from the loads that run beside them.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   constexpr int TILES = 40;
   long long mine = 0;
   int most = 0;
-  Request req{};  // the thread's last request: with up to 575 of them its only one
+  Request req{};  // the thread's last request: with up to 607 of them its only one
   for (int r = r0; r < r1; ++r) {
     req = load_request(p, r, blockIdx.x == 0);
     mine += (head_units<WIN>(p, req) + (WIN ? (long long)req.qn << TILES : 0)) * p.n_kv_head;
@@ -733,7 +733,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   // A window makes work tiles alike, and so few units long that a tile cut in two costs more than it evens out:
   // whole work tiles then, if the most that a CTA gets is within JOIN units of an equal share.  Cut and whole: 64
   // ragged requests (window 1024) 28.8 and 19.3 us, four 2048-token prompts (512) 38.1 and 32.6, 2 x 2011 tokens (4001)
-  // 68.0 and 64.5; 20 requests 17.0 and 18.8, the prompts with a window of 1024 40.9 and 43.9.
+  // 68.0 and 64.5; 20 requests 17.0 and 18.8, the prompts with a window of 1024 40.9 and 43.9 (all with 8 query
+  // heads on 2 key/value heads; other groups have not been measured).
   bool whole = false;
   if constexpr (WIN) {
     const int tiles = (int)(total >> TILES);

@@ -408,7 +408,8 @@ moe_status_t moe_attention_core(const moe_attn_shape_t* shape, const void* qkv, 
  *   trained_len == 0: divided by `factor` (>= 1; 1: none);
  *   trained_len  > 0: divided by `factor` where the pair makes at most slow_turns turns over
  *     trained_len tokens, kept where it makes fast_turns or more, and in between a mixture of
- *     the two frequencies, linear in the turns (0 <= slow_turns < fast_turns).
+ *     the two frequencies, linear in the turns (0 <= slow_turns < fast_turns).  Programs whose mixture is
+ *     linear in the pair's index have other frequencies in between: they put in their own turns.
  * base >= 1.  Other values of turns can be put in by the caller. */
 enum { MOE_ROPE_HALVES = 0, MOE_ROPE_INTERLEAVED = 1 };
 typedef struct {
